@@ -1,0 +1,554 @@
+"""Cases of the softmax-attention operators that stand beside the gated delta rule in a hybrid model,
+with their plain forms: causal attention over whole prompts and its gradients, the plan of a paged
+cache (block table, slots, positions), the write of new tokens into the 8-bit cache, and one-token
+attention over it.
+
+`run` with `own` false computes each operator with elementary torch operations in 32 bits, with
+`own` true through this repository's entry points.  `exact` is the definition in 64 bits.
+
+Shapes: q [.., Hq, d], k and v [.., Hk, d], Hq = G Hk, query head h reads key head h / G; packed
+prompts carry cu_seqlens.  Cache: [pages, Hk, page, d] e4m3 with one power-of-two scale for each
+(page, head): the least 2^e with amax / 2^e <= 448, at least 2^-100.
+"""
+import math
+
+import torch
+
+own = False
+
+E4M3_MAX = 448.0
+SCALE_FLOOR = -100
+
+# The sizes come from the repository's named workloads: tiny (T 256, 2 heads, d 64, fp32), hybrid_lm
+# (8 x 4096, 12 heads on 4 key heads, d 64, bf16), varlen (lengths U[128, 8192], 16 heads, d 128)
+# and decode (256 sequences, 32 heads, d 128).
+_LISTED = [
+    # one short prompt in fp32, as a parity check or a first chat turn runs it: latency counts
+    dict(name="prompt_tiny_f32", op="prompt", dtype="f32", d=64, Hk=1, G=2, n=1, lo=256, hi=256, packed=False),
+    # the attention layers of a hybrid model's training batch, forward
+    dict(name="prompt_hybrid_lm", op="prompt", dtype="bf16", d=64, Hk=4, G=3, n=8, lo=4096, hi=4096, packed=False),
+    # prefill of a serving batch: ragged prompts packed without padding
+    dict(name="prompt_packed", op="prompt", dtype="bf16", d=128, Hk=4, G=4, n=8, lo=128, hi=8192, packed=True),
+    # the same training batch, backward
+    dict(name="grad_hybrid_lm", op="grad", dtype="bf16", d=64, Hk=4, G=3, n=8, lo=4096, hi=4096, packed=False),
+    # fine-tuning on packed documents of different lengths, backward
+    dict(name="grad_packed", op="grad", dtype="bf16", d=128, Hk=4, G=4, n=8, lo=128, hi=4096, packed=True),
+    # every generation step of a serving batch: one new token for each of 256 requests
+    dict(name="plan_decode", op="plan", n=256, page=64, lo=128, hi=8192, new_lo=1, new_hi=1),
+    # admission of a batch of prompts
+    dict(name="plan_prompts", op="plan", n=32, page=64, lo=0, hi=0, new_lo=128, new_hi=8192),
+    # the new keys and values of one generation step
+    dict(name="append_decode", op="append", dtype="bf16", d=128, Hk=8, n=256, page=64, lo=128, hi=2048,
+         new_lo=1, new_hi=1),
+    # the keys and values of a prefilled batch
+    dict(name="append_prompts", op="append", dtype="bf16", d=128, Hk=4, n=32, page=64, lo=0, hi=0,
+         new_lo=128, new_hi=8192),
+    # a single short conversation with fp32 activations: latency counts
+    dict(name="decode_single_f32", op="decode", dtype="f32", d=64, Hk=4, G=3, n=1, page=64, lo=500, hi=500),
+    # one very long context
+    dict(name="decode_long", op="decode", dtype="bf16", d=128, Hk=4, G=4, n=1, page=64, lo=65536, hi=65536),
+    # a full serving batch of ragged contexts
+    dict(name="decode_batch", op="decode", dtype="bf16", d=128, Hk=8, G=4, n=256, page=64, lo=128, hi=8192),
+]
+
+
+def listed():
+    return [dict(c) for c in _LISTED]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["prompt", "grad", "plan", "append", "decode"])
+    c = dict(op=op)
+    if op != "plan":
+        c["dtype"] = rng.choice(["bf16", "bf16", "f32"])
+        c["d"] = rng.choice([64, 128])
+        c["Hk"] = rng.choice([1, 2, 3, 4, 8])
+    if op in ("prompt", "grad"):
+        c["G"] = rng.choice([1, 2, 3, 4, 5, 8])
+        c["n"] = _log(rng, 1, 40)
+        c["packed"] = rng.random() < 0.7
+        # heads x padded length squared, at most the largest listed case's; fp32 (on CUDA cores) less
+        room = 8 * 16 * (8192 if op == "prompt" else 4096) ** 2 // (8 if c["dtype"] == "f32" else 1)
+        top = int(math.sqrt(room / (c["n"] * c["Hk"] * c["G"])))
+        c["hi"] = _log(rng, 16, min(top, 16384))
+        c["lo"] = max(1, int(c["hi"] * rng.choice([0.02, 0.3, 0.9]))) if c["packed"] else c["hi"]
+        return c
+    c["page"] = rng.choice([16, 32, 64, 128])
+    if op == "plan":
+        c["n"] = _log(rng, 1, 2048)
+        prompts = rng.random() < 0.5
+        c["hi"] = _log(rng, 16, 8192)
+        c["lo"] = 0
+        c["new_hi"] = max(1, min(_log(rng, 2, 8192), 200000 // c["n"])) if prompts else 1
+        c["new_lo"] = 0
+        return c
+    if op == "append":
+        prompts = rng.random() < 0.5
+        c["n"] = _log(rng, 1, 64 if prompts else 512)
+        c["lo"], c["hi"] = 0, _log(rng, 2, 2048)
+        c["new_hi"] = max(1, min(_log(rng, 2, 8192), 512 * 1024 // (c["Hk"] * c["n"]))) if prompts else 1
+        c["new_lo"] = 0 if prompts else 1
+        return c
+    c["G"] = rng.choice([1, 2, 3, 4, 8, 16, 20])
+    c["n"] = _log(rng, 1, 256)
+    c["hi"] = _log(rng, 16, min(65536, 256 * 8192 * 8 * 128 // (c["n"] * c["Hk"] * c["d"] * max(1, c["G"] // 4))))
+    c["lo"] = int(c["hi"] * rng.choice([0, 0.3, 0.9]))
+    return c
+
+
+def _dtype(case):
+    return torch.bfloat16 if case["dtype"] == "bf16" else torch.float32
+
+
+def _generators(seed):
+    return torch.Generator().manual_seed(int(seed) * 7919 + 11), torch.Generator("cuda").manual_seed(int(seed) * 104729 + 13)
+
+
+def _lengths(case):
+    """(tokens held or in the prompt, new tokens) of each request: a case has its own set of lengths."""
+    g = torch.Generator().manual_seed(1001 + case["n"] * 31 + case["hi"] * 7 + case.get("new_hi", 0))
+    ints = lambda lo, hi: torch.randint(int(lo), int(hi) + 1, (case["n"],), generator=g)
+    return ints(case["lo"], case["hi"]), ints(case.get("new_lo", 0), case.get("new_hi", 0))
+
+
+def _shuffled(case, g):
+    """The case's lengths in an order of the seed's."""
+    lens, new = _lengths(case)
+    at = torch.randperm(case["n"], generator=g)
+    return lens[at], new[at]
+
+
+def _cu(lens):
+    cu = torch.zeros(len(lens) + 1, dtype=torch.int32)
+    cu[1:] = torch.cumsum(lens, 0).to(torch.int32)
+    return cu
+
+
+def _randn(shape, g, dt):
+    return torch.randn(shape, generator=g, device="cuda").to(dt)
+
+
+def prepare(case, seed):
+    with torch.no_grad():
+        return dict(prompt=_prepare_prompt, grad=_prepare_grad, plan=_prepare_plan, append=_prepare_append,
+                    decode=_prepare_decode)[case["op"]](case, seed)
+
+
+def _prepare_prompt(case, seed):
+    gc, g = _generators(seed)
+    dt, d, Hk, G = _dtype(case), case["d"], case["Hk"], case["G"]
+    s = dict(op=case["op"], cu=None, scale=d ** -0.5)
+    if case["packed"]:
+        lens, _ = _shuffled(case, gc)
+        lead = (int(lens.sum()),)
+        s["cu"] = _cu(lens).cuda()
+        s["longest"] = int(lens.max())
+    else:
+        lead = (case["n"], case["hi"])
+        s["longest"] = case["hi"]
+    # after a norm and a projection: order one, with some correlation between queries and keys so
+    # that the softmax has peaks
+    common = torch.randn(lead + (Hk, 1, d), generator=g, device="cuda")
+    s["q"] = (torch.randn(lead + (Hk, G, d), generator=g, device="cuda") + 0.5 * common).reshape(lead + (Hk * G, d)).to(dt)
+    s["k"] = (torch.randn(lead + (Hk, d), generator=g, device="cuda") + 0.5 * common.squeeze(-2)).to(dt)
+    s["v"] = _randn(lead + (Hk, d), g, dt)
+    return s
+
+
+def _prepare_grad(case, seed):
+    s = _prepare_prompt(case, seed)
+    _, g = _generators(seed + 1)
+    s["dout"] = _randn(tuple(s["q"].shape), g, s["q"].dtype)
+    s["out"], s["lse"] = _plain_prompt(s)  # a training step has the forward's results in hand
+    return s
+
+
+def _table(lens, page, spare, gc):
+    """Block table of requests holding `lens` tokens: shuffled page numbers, -1 where none is held."""
+    blocks = (lens + page - 1) // page
+    held = int(blocks.sum())
+    total = held + int(spare)
+    order = torch.randperm(max(total, 1), generator=gc).to(torch.int32)
+    return blocks, held, total, order
+
+
+def _fill_table(blocks, order, width):
+    at = torch.arange(width)
+    first = torch.cumsum(blocks, 0) - blocks
+    has = at[None, :] < blocks[:, None]
+    return torch.where(has, order[(first[:, None] + at[None, :]).clamp(max=len(order) - 1)], torch.tensor(-1, dtype=torch.int32))
+
+
+def _prepare_plan(case, seed):
+    gc, _ = _generators(seed)
+    n, page = case["n"], case["page"]
+    lens, new = _shuffled(case, gc)
+    width = (case["hi"] + case["new_hi"] + page - 1) // page + 1
+    need = int(((lens + new + page - 1) // page - (lens + page - 1) // page).sum())
+    blocks, held, total, order = _table(lens, page, need + 64, gc)
+    # serving engines size the slot arrays once, for the largest step
+    return dict(op="plan", page=page, rows=int(new.sum()) + 64, lens=lens.to(torch.int32).cuda(),
+                new=new.to(torch.int32).cuda(), table=_fill_table(blocks, order, width).cuda(),
+                free=order[held:].contiguous().cuda(), head=torch.zeros(1, dtype=torch.int32, device="cuda"))
+
+
+def _fp8_cache(pages, Hk, page, d, g):
+    """A filled cache: values of order one with another magnitude for each (page, head)."""
+    q8 = torch.empty(pages, Hk, page, d, dtype=torch.float8_e4m3fn, device="cuda")
+    scale = torch.empty(pages, Hk, device="cuda")
+    step = max(1, (1 << 28) // (Hk * page * d))
+    for a in range(0, pages, step):
+        m = min(step, pages - a)
+        x = torch.randn(m, Hk, page, d, generator=g, device="cuda")
+        x *= torch.exp2(torch.rand(m, Hk, 1, 1, generator=g, device="cuda") * 2 - 1)
+        s = _pow2_scale(x.abs().amax((-1, -2)))
+        q8[a:a + m] = (x / s[..., None, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+        scale[a:a + m] = s
+    return q8, scale
+
+
+def _prepare_append(case, seed):
+    gc, g = _generators(seed)
+    n, page, Hk, d, dt = case["n"], case["page"], case["Hk"], case["d"], _dtype(case)
+    lens, new = _shuffled(case, gc)
+    blocks, held, total, order = _table(lens + new, page, 8, gc)
+    table = _fill_table(blocks, order, int(blocks.max()) + 1)
+    row = torch.repeat_interleave(torch.arange(n), new)
+    pos = torch.arange(int(new.sum())) - (torch.cumsum(new, 0) - new)[row] + lens[row]
+    slots = table[row, pos // page].long() * page + pos % page
+    s = dict(op="append", page=page)
+    s["kc"], s["ks"] = _fp8_cache(total, Hk, page, d, g)
+    s["vc"], s["vs"] = _fp8_cache(total, Hk, page, d, g)
+    # a captured step has a fixed number of rows: the last ones carry no token
+    s["slots"] = torch.cat([slots, torch.full((3,), -1)]).to(torch.int32).cuda()
+    rows = len(s["slots"])
+    s["k"], s["v"] = (_randn((rows, Hk, d), g, torch.float32) * 1.5).to(dt), _randn((rows, Hk, d), g, dt)
+    return s
+
+
+def _prepare_decode(case, seed):
+    gc, g = _generators(seed)
+    n, page, Hk, d, dt = case["n"], case["page"], case["Hk"], case["d"], _dtype(case)
+    lens, _ = _shuffled(case, gc)
+    blocks, held, total, order = _table(lens, page, 8, gc)
+    s = dict(op="decode", page=page, scale=d ** -0.5, lens=lens.to(torch.int32).cuda(), total=int(lens.sum()))
+    s["table"] = _fill_table(blocks, order, max(1, int(blocks.max()))).cuda()
+    s["kc"], s["ks"] = _fp8_cache(total, Hk, page, d, g)
+    s["vc"], s["vs"] = _fp8_cache(total, Hk, page, d, g)
+    s["q"] = _randn((n, Hk * case["G"], d), g, dt)
+    return s
+
+
+def run(s):
+    with torch.no_grad():
+        if own:
+            return _own(s)
+        return dict(prompt=_plain_prompt, grad=_plain_grad, plan=_plain_plan, append=_plain_append,
+                    decode=_plain_decode)[s["op"]](s)
+
+
+def _own(s):
+    import linear_attention_sequence_rule_b200 as gdn
+    if s["op"] == "prompt":
+        return gdn.attn_fwd(s["q"], s["k"], s["v"], cu_seqlens=s["cu"], scale=s["scale"])
+    if s["op"] == "grad":
+        return gdn.attn_bwd(s["q"], s["k"], s["v"], s["out"], s["lse"], s["dout"], cu_seqlens=s["cu"], scale=s["scale"])
+    if s["op"] == "plan":
+        p = gdn.cache_plan(s["lens"], s["new"], s["table"], s["free"], s["head"], s["page"], s["rows"])
+        return (p.cu_seqlens, p.slots, p.positions, s["table"], p.lens, p.free_head, p.status)
+    if s["op"] == "append":
+        gdn.cache_append(s["k"], s["v"], s["slots"], s["kc"], s["vc"], s["ks"], s["vs"])
+        return s["kc"], s["vc"], s["ks"], s["vs"]
+    return gdn.attn_decode(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["lens"], scale=s["scale"])
+
+
+# ---- plain forms --------------------------------------------------------------------------------
+
+def _padded(s):
+    """(token numbers [n, L], which of them exist) of packed prompts; dense ones need neither."""
+    at = torch.arange(s["longest"], device="cuda")
+    idx = s["cu"][:-1, None].long() + at
+    live = at < (s["cu"][1:] - s["cu"][:-1])[:, None]
+    return idx.clamp_(max=len(s["q"]) - 1), live
+
+
+def _scores(s):
+    """Padded fp32 operands [n, Hk, (G) L, d] and exp(score - row maximum), with the rows' sums."""
+    q, k, v = s["q"], s["k"], s["v"]
+    live = None
+    if s["cu"] is not None:
+        idx, live = _padded(s)
+        q, k, v = q[idx], k[idx], v[idx]
+    n, L, Hq, d = q.shape
+    Hk = k.shape[2]
+    q = q.float().permute(0, 2, 1, 3).reshape(n, Hk, Hq // Hk * L, d)
+    k, v = k.float().transpose(1, 2), v.float().transpose(1, 2)
+    p = torch.matmul(q, k.transpose(-1, -2)).view(n, Hk, Hq // Hk, L, L)
+    p *= s["scale"]
+    at = torch.arange(L, device="cuda")
+    p.masked_fill_(at[None, :] > at[:, None], -math.inf)
+    m = p.amax(-1, keepdim=True)
+    p.sub_(m).exp_()
+    return q, k, v, p, m, p.sum(-1, keepdim=True), live
+
+
+def _rows(x, live, heads):
+    """[n, .., L, d] back to the caller's layout [.., heads, d]."""
+    n, L = x.shape[0], x.shape[-2]
+    x = x.reshape(n, heads, L, -1).transpose(1, 2)
+    return x[live] if live is not None else x.contiguous()
+
+
+def _plain_prompt(s):
+    q, k, v, p, m, l, live = _scores(s)
+    n, Hk, G, L, _ = p.shape
+    o = torch.matmul(p.view(n, Hk, G * L, L), v).view(n, Hk, G, L, -1) / l
+    lse = m + l.log()
+    return _rows(o, live, Hk * G).to(s["q"].dtype), _rows(lse, live, Hk * G).squeeze(-1)
+
+
+def _plain_grad(s):
+    q, k, v, p, m, l, live = _scores(s)
+    n, Hk, G, L, _ = p.shape
+    do = s["dout"]
+    if live is not None:
+        do = do[_padded(s)[0]] * live[:, :, None, None]  # rows that do not exist have no gradient
+    do = do.float().permute(0, 2, 1, 3).reshape(n, Hk, G * L, -1)
+    p /= l
+    p = p.view(n, Hk, G * L, L)
+    dv = torch.matmul(p.transpose(-1, -2), do)
+    dp = torch.matmul(do, v.transpose(-1, -2))
+    ds = dp.sub_((p * dp).sum(-1, keepdim=True)).mul_(p)
+    dq = torch.matmul(ds, k) * s["scale"]
+    dk = torch.matmul(ds.transpose(-1, -2), q) * s["scale"]
+    dt = s["q"].dtype
+    return (_rows(dq.view(n, Hk * G, L, -1), live, Hk * G).to(dt), _rows(dk, live, Hk).to(dt),
+            _rows(dv, live, Hk).to(dt))
+
+
+def _plain_plan(s):
+    lens, new, page, table = s["lens"].long(), s["new"].long(), s["page"], s["table"]
+    rows, dev = s["rows"], lens.device
+    held, want = (lens + page - 1) // page, (lens + new + page - 1) // page
+    more = want - held
+    first = torch.cumsum(more, 0) - more  # entries of the free list that earlier requests take
+    at = torch.arange(table.shape[1], device=dev)
+    fresh = (at >= held[:, None]) & (at < want[:, None])
+    pick = (s["head"].long() + first[:, None] + at - held[:, None]).clamp(0, len(s["free"]) - 1)
+    table.copy_(torch.where(fresh, s["free"][pick], table))
+    end = torch.cumsum(new, 0)
+    cu = torch.cat([end.new_zeros(1), end])
+    t = torch.arange(rows, device=dev)
+    row = torch.searchsorted(end, t, right=True).clamp(max=len(new) - 1)
+    pos = t - cu[row] + lens[row]
+    slots = table[row, (pos // page).clamp(0, table.shape[1] - 1)].long() * page + pos % page
+    none = t >= end[-1]
+    i32 = torch.int32
+    return (cu.to(i32), slots.masked_fill(none, -1).to(i32), pos.masked_fill(none, -1).to(i32), table,
+            (lens + new).to(i32), (s["head"] + more.sum()).to(i32), torch.zeros(2, dtype=i32, device=dev))
+
+
+def _pow2_scale(amax):
+    """The least power of two 2^e, e >= -100, with amax / 2^e <= 448 (= 1.75 x 2^8)."""
+    mant, exp = torch.frexp(amax)  # amax = mant 2^exp, mant in [0.5, 1)
+    e = torch.where(mant <= 0.875, exp - 9, exp - 8)
+    e = torch.where(amax > 0, e, torch.full_like(e, SCALE_FLOOR)).clamp(min=SCALE_FLOOR)
+    return torch.ldexp(torch.ones_like(amax), e)
+
+
+def _plain_append(s):
+    slots, page = s["slots"].long(), s["page"]
+    # tokens that lie in one page are neighbours: one run each
+    tok = (slots >= 0).nonzero().squeeze(1)
+    slot = slots[tok]
+    starts = torch.ones_like(slot, dtype=torch.bool)
+    starts[1:] = slot[1:] // page != slot[:-1] // page
+    run = torch.cumsum(starts, 0) - 1
+    head = slot[starts]
+    pages, off = head // page, head % page
+    held = torch.arange(page, device="cuda") < off[:, None]
+    for x, cache, scale in ((s["k"], s["kc"], s["ks"]), (s["v"], s["vc"], s["vs"])):
+        x = x[tok].float()
+        Hk, d = x.shape[1:]
+        was = torch.where(held.any(1)[:, None], scale[pages], torch.zeros_like(scale[pages]))
+        block = torch.where(held[:, None, :, None], cache[pages].float() * was[..., None, None], 0.0)
+        top = torch.zeros(len(pages), Hk, device="cuda")
+        top.index_reduce_(0, run, x.abs().amax(-1), "amax")
+        to = torch.maximum(was, _pow2_scale(top))
+        block[run, :, slot % page] = x
+        q8 = (block / to[..., None, None]).clamp_(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+        wrote = held.clone()
+        wrote[run, slot % page] = True
+        bytes_ = cache.view(torch.uint8)
+        bytes_[pages] = torch.where(wrote[:, None, :, None], q8.view(torch.uint8), bytes_[pages])
+        scale[pages] = to
+    return s["kc"], s["vc"], s["ks"], s["vs"]
+
+
+def _plain_decode(s):
+    q, table, lens = s["q"].float(), s["table"], s["lens"]
+    n, Hq, d = q.shape
+    Hk, page = s["kc"].shape[1:3]
+    pages = table.clamp(min=0).long()
+    width = pages.shape[1]
+
+    def gather(cache, scale):
+        x = cache.view(torch.uint8)[pages].view(torch.float8_e4m3fn).float()
+        x *= scale[pages][..., None, None]
+        return x.transpose(1, 2).reshape(n, Hk, width * page, d)
+
+    k = gather(s["kc"], s["ks"])
+    p = torch.matmul(q.view(n, Hk, Hq // Hk, d), k.transpose(-1, -2)) * s["scale"]
+    del k
+    none = torch.arange(width * page, device="cuda") >= lens[:, None]
+    p.masked_fill_(none[:, None, None, :], -math.inf)
+    m = p.amax(-1, keepdim=True).clamp(min=-3e38)
+    p = p.sub_(m).exp_()
+    l = p.sum(-1, keepdim=True)
+    v = gather(s["vc"], s["vs"])
+    o = torch.matmul(p, v) / torch.where(l > 0, l, torch.ones_like(l))
+    return o.view(n, Hq, d).to(s["q"].dtype)
+
+
+# ---- work ---------------------------------------------------------------------------------------
+
+def work(case):
+    op, (lens, new) = case["op"], _lengths(case)
+    tokens, more = int(lens.sum()), int(new.sum())
+    if op == "plan":
+        page = case["page"]
+        taken = int(((lens + new + page - 1) // page - (lens + page - 1) // page).sum())
+        # lengths in and out, offsets, slots and positions, the pages taken and their table entries
+        return dict(bytes=16 * case["n"] + 8 * more + 8 * taken, flops=8 * case["n"] + 4 * more)
+    e, Hk, d = (2 if case["dtype"] == "bf16" else 4), case["Hk"], case["d"]
+    if op == "append":
+        page = case["page"]
+        touched = int(((lens + new + page - 1) // page - lens // page)[new > 0].sum())
+        # each new row in and out, the slots, and a scale in and out for each page touched
+        return dict(bytes=more * (2 * Hk * d * (e + 1) + 4) + 16 * Hk * touched, flops=4 * more * Hk * d)
+    Hq = Hk * case["G"]
+    if op == "decode":
+        page = case["page"]
+        blocks = int(((lens + page - 1) // page).sum())
+        # the cache, its scales and the table in, q in and the result out
+        return dict(bytes=tokens * 2 * Hk * d + blocks * (8 * Hk + 4) + 2 * case["n"] * Hq * d * e,
+                    flops=4 * tokens * Hq * d)
+    pairs = int((lens * (lens + 1) // 2).sum())
+    if op == "prompt":  # two products; q, k, v in, out and the log sums out
+        return dict(bytes=tokens * (e * d * (2 * Hq + 2 * Hk) + 4 * Hq), flops=4 * Hq * pairs * d)
+    # five products; q, k, v, out, dout and the log sums in, three gradients out
+    return dict(bytes=tokens * (e * d * (4 * Hq + 4 * Hk) + 4 * Hq), flops=10 * Hq * pairs * d)
+
+
+# ---- the definitions in 64 bits -------------------------------------------------------------------
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    with torch.no_grad():
+        return dict(prompt=_exact_prompt, grad=_exact_prompt, plan=lambda s: None, append=_exact_append,
+                    decode=_exact_decode)[case["op"]](s)
+
+
+def _exact_prompt(s):
+    """One (sequence, query head) at a time."""
+    q, k, v = s["q"], s["k"], s["v"]
+    Hq, d = q.shape[-2:]
+    G = Hq // k.shape[-2]
+    grad = s["op"] == "grad"
+    flat = lambda x: x.reshape(-1, *x.shape[-2:])
+    q, k, v = flat(q), flat(k), flat(v)
+    if s["cu"] is None:
+        L = s["longest"]
+        bounds = [(a, a + L) for a in range(0, len(q), L)]
+    else:
+        c = s["cu"].tolist()
+        bounds = list(zip(c[:-1], c[1:]))
+    f = dict(dtype=torch.float64, device="cuda")
+    out, lse = torch.zeros(q.shape, **f), torch.zeros(q.shape[:2], **f)
+    dq, dk, dv = torch.zeros(q.shape, **f), torch.zeros(k.shape, **f), torch.zeros(v.shape, **f)
+    do_all = flat(s["dout"]) if grad else None
+    for a, b in bounds:
+        upper = torch.ones(b - a, b - a, dtype=torch.bool, device="cuda").triu(1)
+        for h in range(Hq):
+            qh, kh, vh = (x[a:b, i].double() for x, i in ((q, h), (k, h // G), (v, h // G)))
+            w = qh @ kh.T * s["scale"]
+            w[upper] = -math.inf
+            z = torch.logsumexp(w, -1)
+            w = torch.exp_(w.sub_(z[:, None]))
+            o = w @ vh
+            if not grad:
+                out[a:b, h], lse[a:b, h] = o, z
+                continue
+            do = do_all[a:b, h].double()
+            dv[a:b, h // G] += w.T @ do
+            t = do @ vh.T
+            t.sub_((do * o).sum(-1, keepdim=True)).mul_(w)
+            dq[a:b, h] = t @ kh * s["scale"]
+            dk[a:b, h // G] += t.T @ qh * s["scale"]
+    if grad:
+        return dq.view(s["q"].shape), dk.view(s["k"].shape), dv.view(s["v"].shape)
+    return out.view(s["q"].shape), lse.view(s["q"].shape[:-1])
+
+
+def _exact_append(s):
+    """The stored values and scales, one run of tokens at a time, from the written definition."""
+    page = s["page"]
+    slots = s["slots"].tolist()
+    if len(slots) > 200000:
+        return None
+    res = []
+    for x, cache, scale in ((s["k"], s["kc"], s["ks"]), (s["v"], s["vc"], s["vs"])):
+        val = cache.double()
+        sc = scale.double()
+        x = x.double()
+        t = 0
+        while t < len(slots):
+            if slots[t] < 0:
+                t += 1
+                continue
+            u = t + 1
+            while u < len(slots) and slots[u] >= 0 and slots[u] // page == slots[t] // page:
+                u += 1
+            pg, off = slots[t] // page, slots[t] % page
+            top = x[t:u].abs().amax((0, 2))
+            # smallest power of two that holds the largest magnitude below 448
+            need = torch.exp2(torch.ceil(torch.log2((top / E4M3_MAX).clamp(min=2.0 ** SCALE_FLOOR))))
+            need = torch.where(top > need * E4M3_MAX, need * 2, need)
+            old = sc[pg] if off else torch.zeros_like(need)
+            fin = torch.maximum(old, need)
+            if off:
+                val[pg, :, :off] = _round_e4m3(val[pg, :, :off] * (old / fin)[:, None, None])
+            val[pg, :, off:off + u - t] = _round_e4m3((x[t:u] / fin[None, :, None]).transpose(0, 1))
+            sc[pg] = fin
+            t = u
+        res.append((val, sc))
+    return res[0][0], res[1][0], res[0][1], res[1][1]
+
+
+def _round_e4m3(x):
+    """Nearest e4m3 value, ties to even: 3 mantissa bits, steps of 2^-9 below 2^-6."""
+    _, e = torch.frexp(x.abs().clamp(min=2.0 ** -6))
+    step = torch.exp2((e - 4).double())
+    return (torch.round(x / step) * step).clamp(-E4M3_MAX, E4M3_MAX)
+
+
+def _exact_decode(s):
+    """One request at a time."""
+    q, table, page = s["q"], s["table"].long(), s["page"]
+    n, Hq, d = q.shape
+    Hk = s["kc"].shape[1]
+    out = torch.zeros(n, Hq, d, dtype=torch.float64, device="cuda")
+    for i, L in enumerate(s["lens"].tolist()):
+        if L == 0:
+            continue
+        pages = table[i, :(L + page - 1) // page]
+        full = lambda c, sc: (c.view(torch.uint8)[pages].view(torch.float8_e4m3fn).to(torch.float64)
+                              * sc[pages].double()[..., None, None]).permute(1, 0, 2, 3).reshape(Hk, -1, d)[:, :L]
+        k, v = full(s["kc"], s["ks"]), full(s["vc"], s["vs"])
+        w = torch.einsum("hgd,htd->hgt", q[i].double().view(Hk, Hq // Hk, d), k) * s["scale"]
+        out[i] = torch.einsum("hgt,htd->hgd", torch.softmax(w, -1), v).reshape(Hq, d)
+    return out
