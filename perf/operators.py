@@ -8,7 +8,7 @@ attention over it.
 
 Shapes: q [.., Hq, d], k and v [.., Hk, d], Hq = G Hk, query head h reads key head h / G; packed
 prompts carry cu_seqlens.  Cache: [pages, Hk, page, d] e4m3 with one power-of-two scale for each
-(page, head): the least 2^e with amax / 2^e <= 448, at least 2^-100.
+(page, head): the least 2^e with amax / 2^e <= 448, at least 2^-60.
 """
 import math
 
@@ -17,7 +17,7 @@ import torch
 own = False
 
 E4M3_MAX = 448.0
-SCALE_FLOOR = -100
+SCALE_FLOOR = -60
 
 # The sizes come from the repository's named workloads: tiny (T 256, 2 heads, d 64, fp32), hybrid_lm
 # (8 x 4096, 12 heads on 4 key heads, d 64, bf16), varlen (lengths U[128, 8192], 16 heads, d 128)
@@ -353,7 +353,7 @@ def _plain_plan(s):
 
 
 def _pow2_scale(amax):
-    """The least power of two 2^e, e >= -100, with amax / 2^e <= 448 (= 1.75 x 2^8)."""
+    """The least power of two 2^e, e >= -60, with amax / 2^e <= 448 (= 1.75 x 2^8)."""
     mant, exp = torch.frexp(amax)  # amax = mant 2^exp, mant in [0.5, 1)
     e = torch.where(mant <= 0.875, exp - 9, exp - 8)
     e = torch.where(amax > 0, e, torch.full_like(e, SCALE_FLOOR)).clamp(min=SCALE_FLOOR)
