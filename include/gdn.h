@@ -384,6 +384,120 @@ GDN_API int gdn_decode_step_gva(const void *q, const void *k, const void *v, con
                                 int dk, int dv, int dtype, void *stream);
 
 /*
+ * ---- Softmax attention of the hybrid models' attention layers -----------------------------------
+ *
+ * A hybrid model runs one softmax-attention layer after every few recurrence layers (Sykra README,
+ * "Architectural Highlights": a 3:1 periodic schedule, grouped-query attention).  The entries below
+ * are that layer's counterparts of gdn_chunk_fwd, gdn_chunk_bwd and gdn_decode_step: attention over
+ * whole prompts, its gradients, and one-token attention over a paged 8-bit cache, with the cache's
+ * planning and writing.  Hq query heads share Hk key/value heads (Hq a multiple of Hk): query head
+ * h reads key head h / (Hq / Hk).  The pages name these layers and give no kernel.
+ */
+
+/*
+ * gdn_attn_fwd -- causal softmax attention over whole prompts.  Per (sequence, query head):
+ *     s_ij = scale q_i . k_j  (j <= i),   lse_i = log sum_j exp(s_ij),
+ *     out_i = sum_j exp(s_ij - lse_i) v_j
+ * Layouts as gdn_chunk_fwd: dense q, out [B,T,Hq,d], k, v [B,T,Hk,d]; packed (cu_seqlens: DEVICE
+ * int32 [B+1], from 0, non-decreasing, at most T) q, out [T,Hq,d], k, v [T,Hk,d].  lse [.., Hq] fp32,
+ * or NULL: not written.  Rows of a packed call behind cu[B] are neither read for any result nor
+ * written.  d in {64, 128}; dtype bf16 (products on the tensor cores with fp32 accumulation, the
+ * softmax in fp32, its weights rounded to bf16 for the second product) or fp32 (CUDA cores, fp32
+ * throughout).  scale finite and > 0.  A sequence may have length 0.  A non-finite k or v row may
+ * also reach earlier rows of the same sequence within its block of 128 tokens, never another
+ * sequence.  No workspace.  Errors as gdn_chunk_fwd.
+ */
+GDN_API int gdn_attn_fwd(const void *q, const void *k, const void *v, void *out, float *lse, int B, int T, int Hq,
+                         int Hk, int d, const int32_t *cu_seqlens, int dtype, float scale, void *stream);
+
+/*
+ * gdn_attn_bwd -- gradients of gdn_attn_fwd: given its inputs, its results out and lse, and
+ * dout = dL/dout, it writes dq [.., Hq, d], dk and dv [.., Hk, d], all in dtype:
+ *     p_ij = exp(s_ij - lse_i),  D_i = dout_i . out_i,  ds_ij = p_ij (dout_i . v_j - D_i)
+ *     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
+ * with dk and dv summed over the query heads that share a key head, in a fixed order (no atomics:
+ * a call repeats bit for bit).  Sums are fp32; with bf16 p and ds are rounded to bf16 for the
+ * products they enter.  Rows behind cu[B] are left as they were.  Workspace:
+ * gdn_attn_bwd_workspace_bytes(...) bytes of device memory, 256-byte aligned.  Errors as
+ * gdn_attn_fwd.
+ */
+GDN_API int gdn_attn_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse,
+                         const void *dout, void *dq, void *dk, void *dv, int B, int T, int Hq, int Hk, int d,
+                         const int32_t *cu_seqlens, int dtype, float scale, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* Workspace gdn_attn_bwd needs for these sizes; (size_t)-1 for sizes it rejects. */
+GDN_API size_t gdn_attn_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d, int varlen, int dtype);
+
+/*
+ * gdn_cache_plan -- one step's plan of a paged cache, built on the device from request lengths: N
+ * requests hold lens[r] tokens and get added[r] >= 0 more; the pages the new tokens need are taken
+ * from free_list, in the order of the requests and of their blocks.
+ *   in:  lens, added [N]; free_list [num_free] page numbers; free_head [1]: how many entries of
+ *        free_list are taken already
+ *   in and out: block_table [N, max_blocks]: entry b of row r is the page of the request's tokens
+ *        b page .. b page + page - 1.  Entries of pages already held are read, those of the pages
+ *        taken now are written, all others are left as they were.
+ *   out: cu_seqlens [N+1]: offsets of the requests' new tokens in the step's packed rows;
+ *        slots [rows]: page number x page + offset of every new token, positions [rows]: its
+ *        position in its request; both -1 in rows behind cu_seqlens[N]
+ *        lens_out [N] = lens + added, free_head_out [1] (each may be the input array itself)
+ *        status [2]: {0, 0}; or why the whole plan was refused, in which case no page is taken, the
+ *        table is left, cu_seqlens is all 0, slots and positions all -1, lens_out = lens and
+ *        free_head_out = free_head: {1, pages lacking}, {2, the first request with a negative
+ *        length or more tokens than its table row holds}, {3, new tokens beyond rows, or 2^31 - 1},
+ *        {4, 0}: free_head outside 0 .. num_free.  The first of 4, 2, 3, 1 that applies is given.
+ * All int32.  1 <= N <= 16384, page in {16, 32, 64, 128}, max_blocks >= 1, max_blocks page < 2^31,
+ * num_free >= 0, rows >= 0.  One launch, no workspace; arrays must not overlap but as named above.
+ */
+GDN_API int gdn_cache_plan(const int32_t *lens, const int32_t *added, int32_t *block_table,
+                           const int32_t *free_list, const int32_t *free_head, int32_t *cu_seqlens,
+                           int32_t *slots, int32_t *positions, int32_t *lens_out, int32_t *free_head_out,
+                           int32_t *status, int N, int max_blocks, int num_free, int rows, int page,
+                           void *stream);
+
+/*
+ * gdn_cache_append -- write new keys and values into a paged 8-bit cache.  k, v [rows, Hk, d] in
+ * dtype; slots [rows] int32 as gdn_cache_plan gives them (a slot outside 0 .. num_pages page - 1
+ * carries no token); k_cache, v_cache [num_pages, Hk, page, d] e4m3; k_scale, v_scale
+ * [num_pages, Hk] fp32.  A stored value stands for value x scale of its (page, head).
+ * Rows that go to the same page stand next to each other, with consecutive slots, as in a plan.  Per
+ * page touched and head, with `first` the offset of the first new row in the page: the offsets
+ * before `first` hold tokens already (none if first = 0, and the page's old scale is forgotten).
+ * The new scale is the larger of the old one and of the least power of two 2^e, e >= -60, with
+ * max |new values| <= 448 2^e; tokens held are rounded again where the scale grew (exact but for
+ * values that fall below e4m3's normal range), new ones are divided by it and rounded to nearest
+ * even.  Infinities are stored as the largest finite value, NaN as NaN.  Offsets after the new rows
+ * and pages not touched are left as they were.  d in {64, 128}, page in {16, 32, 64, 128},
+ * num_pages page < 2^31; rows = 0 does nothing.  No workspace.
+ */
+GDN_API int gdn_cache_append(const void *k, const void *v, const int32_t *slots, void *k_cache, void *v_cache,
+                             float *k_scale, float *v_scale, int rows, int Hk, int d, int page, int num_pages,
+                             int dtype, void *stream);
+
+/*
+ * gdn_attn_decode -- one generation step's attention: one query token per request over its cached
+ * tokens.  q, out [N, Hq, d] in dtype; caches and scales as gdn_cache_append writes them (scales
+ * finite and >= 0; a value scale below 2^-60 is taken as 2^-60); block_table [N, max_blocks] and
+ * lens [N] int32 as gdn_cache_plan gives them (lens includes the token just appended):
+ *     out[n,h] = sum_{j < lens[n]} softmax_j(scale q[n,h] . K[n,j,h/G]) V[n,j,h/G],   G = Hq / Hk
+ * A request of length <= 0 gets zeros; lengths beyond max_blocks page are cut there; tokens whose
+ * table entry is outside 0 .. num_pages - 1 are left out.  Cache contents beyond a request's length
+ * are never part of a result, whatever they are.  Cached values enter the tensor cores as fp16
+ * (exact), q as fp16 after a power-of-two scaling (bf16 exact over 22 binary orders; fp32 as a sum
+ * of two fp16), softmax weights as fp16 (bf16 calls) or a sum of two fp16 (fp32 calls), sums in
+ * fp32.  d in {64, 128}; scale finite and > 0.  Workspace: gdn_attn_decode_workspace_bytes(...)
+ * bytes, 256-byte aligned (long contexts are split over CTAs; may be NULL when that is 0).
+ */
+GDN_API int gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                            const float *v_scale, const int32_t *block_table, const int32_t *lens, void *out,
+                            int N, int Hq, int Hk, int d, int page, int num_pages, int max_blocks, int dtype,
+                            float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace gdn_attn_decode needs for these sizes on the CURRENT device; (size_t)-1 for sizes it rejects. */
+GDN_API size_t gdn_attn_decode_workspace_bytes(int N, int Hq, int Hk, int d, int page, int max_blocks, int dtype);
+
+/*
  * gdn_device_status -- synchronise `stream`, then report whether any kernel of this library
  * recorded a device-side failure since the previous call (a bounded wait on an mbarrier that ran
  * out, after which the kernel stopped issuing work and returned): GDN_ERR_TIMEOUT if so, GDN_OK

@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -37,6 +38,9 @@ __all__ = [
     "gdn_decode_step", "gdn_decode_step_fused", "decode_step_fused", "gdn_decode_step_gva", "gdn_chunk_bwd", "gdn_chunk_bwd_workspace_bytes", "gdn_chunk_fwd_workspace_bytes", "gdn_status_string",
     "gdn_last_error", "gdn_version", "gdn_device_status", "gdn_selftest_wait_timeout", "device_status", "chunk_fwd", "chunk_fwd_fused",
     "chunk_fwd_gva", "chunk_bwd", "decode_step", "decode_step_gva", "workspace_bytes",
+    "gdn_attn_fwd", "gdn_attn_bwd", "gdn_attn_bwd_workspace_bytes", "gdn_cache_plan", "gdn_cache_append",
+    "gdn_attn_decode", "gdn_attn_decode_workspace_bytes",
+    "attn_fwd", "attn_bwd", "cache_plan", "CachePlan", "cache_append", "attn_decode",
 ]
 
 GDN_OK = 0
@@ -104,6 +108,20 @@ _lib.gdn_decode_step.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, 
 _lib.gdn_decode_step.restype = _i
 _lib.gdn_decode_step_fused.argtypes = [_vp] * 7 + [_i] * 5 + [ctypes.c_float, ctypes.c_float, _vp]
 _lib.gdn_decode_step_fused.restype = _i
+_lib.gdn_attn_fwd.argtypes = [_vp] * 5 + [_i] * 5 + [_vp, _i, ctypes.c_float, _vp]
+_lib.gdn_attn_fwd.restype = _i
+_lib.gdn_attn_bwd.argtypes = [_vp] * 9 + [_i] * 5 + [_vp, _i, ctypes.c_float, _vp, _sz, _vp]
+_lib.gdn_attn_bwd.restype = _i
+_lib.gdn_attn_bwd_workspace_bytes.argtypes = [_i] * 7
+_lib.gdn_attn_bwd_workspace_bytes.restype = _sz
+_lib.gdn_cache_plan.argtypes = [_vp] * 11 + [_i] * 5 + [_vp]
+_lib.gdn_cache_plan.restype = _i
+_lib.gdn_cache_append.argtypes = [_vp] * 7 + [_i] * 6 + [_vp]
+_lib.gdn_cache_append.restype = _i
+_lib.gdn_attn_decode.argtypes = [_vp] * 8 + [_i] * 8 + [ctypes.c_float, _vp, _sz, _vp]
+_lib.gdn_attn_decode.restype = _i
+_lib.gdn_attn_decode_workspace_bytes.argtypes = [_i] * 7
+_lib.gdn_attn_decode_workspace_bytes.restype = _sz
 _lib.gdn_selftest_wait_timeout.argtypes = [_i, _vp]
 _lib.gdn_selftest_wait_timeout.restype = _i
 _lib.gdn_device_status.argtypes = [_vp]
@@ -214,6 +232,42 @@ def gdn_decode_step_fused(q_raw, k_raw, v, a_raw, b_raw, S_inout, out, N, H, dk,
                           stream) -> int:
     return _lib.gdn_decode_step_fused(q_raw, k_raw, v, a_raw, b_raw, S_inout, out, N, H, dk, dv, dtype, a_scale,
                                       b_scale, stream)
+
+
+def gdn_attn_fwd(q, k, v, out, lse, B, T, Hq, Hk, d, cu_seqlens, dtype, scale, stream) -> int:
+    return _lib.gdn_attn_fwd(q, k, v, out, lse, B, T, Hq, Hk, d, cu_seqlens, dtype, scale, stream)
+
+
+def gdn_attn_bwd(q, k, v, out, lse, dout, dq, dk, dv, B, T, Hq, Hk, d, cu_seqlens, dtype, scale, workspace,
+                 workspace_bytes, stream) -> int:
+    return _lib.gdn_attn_bwd(q, k, v, out, lse, dout, dq, dk, dv, B, T, Hq, Hk, d, cu_seqlens, dtype, scale,
+                             workspace, workspace_bytes, stream)
+
+
+def gdn_attn_bwd_workspace_bytes(B, T, Hq, Hk, d, varlen, dtype) -> int:
+    return _lib.gdn_attn_bwd_workspace_bytes(B, T, Hq, Hk, d, varlen, dtype)
+
+
+def gdn_cache_plan(lens, added, block_table, free_list, free_head, cu_seqlens, slots, positions, lens_out,
+                   free_head_out, status, N, max_blocks, num_free, rows, page, stream) -> int:
+    return _lib.gdn_cache_plan(lens, added, block_table, free_list, free_head, cu_seqlens, slots, positions,
+                               lens_out, free_head_out, status, N, max_blocks, num_free, rows, page, stream)
+
+
+def gdn_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, rows, Hk, d, page, num_pages, dtype,
+                     stream) -> int:
+    return _lib.gdn_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, rows, Hk, d, page, num_pages,
+                                 dtype, stream)
+
+
+def gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, out, N, Hq, Hk, d, page, num_pages,
+                    max_blocks, dtype, scale, workspace, workspace_bytes, stream) -> int:
+    return _lib.gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, out, N, Hq, Hk, d, page,
+                                num_pages, max_blocks, dtype, scale, workspace, workspace_bytes, stream)
+
+
+def gdn_attn_decode_workspace_bytes(N, Hq, Hk, d, page, max_blocks, dtype) -> int:
+    return _lib.gdn_attn_decode_workspace_bytes(N, Hq, Hk, d, page, max_blocks, dtype)
 
 
 def gdn_selftest_wait_timeout(limit_ms, stream) -> int:
@@ -792,4 +846,231 @@ def decode_step_fused(q_raw, k_raw, v, a_raw, b_raw, a_scale, b_scale, S, out=No
                                N, H, dk, dv, _DT[dt], float(a_scale), float(b_scale), _stream_ptr(stream))
     if rc != GDN_OK:
         raise GdnError(rc, gdn_last_error())
+    return out
+
+
+# ---- softmax attention of the hybrid models' attention layers -----------------------------------
+
+class CachePlan(NamedTuple):
+    """What ``cache_plan`` gives beside the block table: offsets of the new tokens, their slots and
+    positions, the lengths after the step, how much of the free list is taken, and the status."""
+    cu_seqlens: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    lens: torch.Tensor
+    free_head: torch.Tensor
+    status: torch.Tensor
+
+
+class _On:
+    """The call's device and stream: the tensors' device is made the current one for the launch, and
+    without a stream the call goes to that device's current stream.  Scratch that a call takes from
+    the allocator is kept from reuse until the stream given has passed it."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"tensors are on {device}, expected a CUDA device")
+        self.device, self.given = device, stream
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        if self.stream.device != device:
+            raise ValueError(f"stream is on {self.stream.device}, the tensors on {device}")
+
+    def call(self, fn, *args):
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(*args, self.stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, self.stream.cuda_stream)
+        if rc != GDN_OK:
+            raise GdnError(rc, gdn_last_error())
+
+    def query(self, fn, *args):
+        with torch.cuda.device(self.device):
+            n = fn(*args)
+        if n == ctypes.c_size_t(-1).value:
+            raise GdnError(GDN_ERR_INVALID_ARGUMENT, gdn_last_error())
+        return n
+
+    def new(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.given is not None:
+            t.record_stream(self.given)
+        return t
+
+    def scratch(self, workspace, need):
+        """(pointer, bytes) of the caller's workspace or of one taken for this call (the third item
+        keeps it alive until the launch)."""
+        if workspace is None and need:
+            workspace = self.new((need,), torch.uint8)
+        if workspace is None:
+            return None, 0, None
+        _need(workspace, "workspace", device=self.device)
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _heads(q, k, cu_seqlens, d_names=("q", "k")):
+    """(lead dims, B, T, Hq, Hk, d, dtype code) of a prompt call."""
+    want = 4 if cu_seqlens is None else 3
+    if q is None or q.dim() != want or k is None or k.dim() != want:
+        raise ValueError(f"{d_names[0]} and {d_names[1]} must have {want} dimensions")
+    if q.dtype not in _DT:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    lead = tuple(q.shape[:-2])
+    if cu_seqlens is None:
+        B, T = lead
+    else:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must hold B + 1 >= 2 offsets")
+        B, T = cu_seqlens.shape[0] - 1, lead[0]
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), q.device)
+    return lead, B, T, q.shape[-2], k.shape[-2], q.shape[-1]
+
+
+def _scale(scale, d):
+    return d ** -0.5 if scale is None else float(scale)
+
+
+def attn_fwd(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None, stream=None):
+    """Causal softmax attention over whole prompts.  Dense q [B,T,Hq,d], k, v [B,T,Hk,d], or packed
+    q [T,Hq,d] ... with cu_seqlens (int32 [B+1] on the device); Hq a multiple of Hk; scale defaults to
+    1 / sqrt(d).  Returns (out, lse), lse [.., Hq] the log of each row's softmax sum.  Rows behind the
+    last sequence of a pack are not written."""
+    lead, B, T, Hq, Hk, d = _heads(q, k, cu_seqlens)
+    dt, on = q.dtype, _On(q.device, stream)
+    _need(q, "q", dt, (*lead, Hq, d))
+    _need(k, "k", dt, (*lead, Hk, d), q.device)
+    _need(v, "v", dt, (*lead, Hk, d), q.device)
+    out = on.new((*lead, Hq, d), dt) if out is None else out
+    lse = on.new((*lead, Hq), torch.float32) if lse is None else lse
+    _need(out, "out", dt, (*lead, Hq, d), q.device)
+    _need(lse, "lse", torch.float32, (*lead, Hq), q.device)
+    if lead.count(0) and cu_seqlens is not None:
+        return out, lse
+    on.call(gdn_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, T, Hq, Hk, d,
+            _ptr(cu_seqlens), _DT[dt], _scale(scale, d))
+    return out, lse
+
+
+def attn_bwd(q, k, v, out, lse, dout, cu_seqlens=None, scale=None, dq=None, dk=None, dv=None, workspace=None,
+             stream=None):
+    """Gradients (dq, dk, dv), in q's dtype, of ``attn_fwd``'s out with respect to q, k and v, from its
+    inputs, its results out and lse, and dout = dL/dout."""
+    lead, B, T, Hq, Hk, d = _heads(q, k, cu_seqlens)
+    dt, dev, on = q.dtype, q.device, _On(q.device, stream)
+    _need(q, "q", dt, (*lead, Hq, d))
+    _need(k, "k", dt, (*lead, Hk, d), dev)
+    _need(v, "v", dt, (*lead, Hk, d), dev)
+    _need(out, "out", dt, (*lead, Hq, d), dev)
+    _need(dout, "dout", dt, (*lead, Hq, d), dev)
+    _need(lse, "lse", torch.float32, (*lead, Hq), dev)
+    dq = on.new((*lead, Hq, d), dt) if dq is None else dq
+    dk = on.new((*lead, Hk, d), dt) if dk is None else dk
+    dv = on.new((*lead, Hk, d), dt) if dv is None else dv
+    _need(dq, "dq", dt, (*lead, Hq, d), dev)
+    _need(dk, "dk", dt, (*lead, Hk, d), dev)
+    _need(dv, "dv", dt, (*lead, Hk, d), dev)
+    if lead.count(0) and cu_seqlens is not None:
+        return dq, dk, dv
+    need = on.query(gdn_attn_bwd_workspace_bytes, B, T, Hq, Hk, d, int(cu_seqlens is not None), _DT[dt])
+    ws, wbytes, _keep = on.scratch(workspace, need)
+    on.call(gdn_attn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, T, Hq, Hk, d, _ptr(cu_seqlens), _DT[dt],
+            _scale(scale, d), ws, wbytes)
+    return dq, dk, dv
+
+
+def cache_plan(lens, added, block_table, free_list, free_head, page, rows, cu_seqlens=None, slots=None,
+               positions=None, lens_out=None, free_head_out=None, status=None, stream=None):
+    """Plan one step of a paged cache on the device: N requests holding ``lens`` tokens get ``added``
+    new ones; pages come from ``free_list`` (entries from free_head on) and go into ``block_table``
+    [N, max_blocks], in place.  ``rows``: how many packed rows the step has room for.  All int32.
+    Returns a CachePlan; a plan that does not fit is refused as a whole (its status is not 0)."""
+    i32, dev, on = torch.int32, lens.device, _On(lens.device, stream)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have 2 dimensions")
+    N, max_blocks = block_table.shape
+    _need(lens, "lens", i32, (N,))
+    _need(added, "added", i32, (N,), dev)
+    _need(block_table, "block_table", i32, (N, max_blocks), dev)
+    _need(free_list, "free_list", i32, (free_list.numel(),), dev)
+    _need(free_head, "free_head", i32, (1,), dev)
+    rows = int(rows)
+    if rows < 0:
+        raise ValueError("rows must be >= 0")
+    given = dict(cu_seqlens=(cu_seqlens, (N + 1,)), slots=(slots, (rows,)), positions=(positions, (rows,)),
+                 lens_out=(lens_out, (N,)), free_head_out=(free_head_out, (1,)), status=(status, (2,)))
+    o = {}
+    for name, (t, shape) in given.items():
+        if t is None:
+            o[name] = on.new(shape, i32)
+        else:
+            _need(t, name, i32, shape, dev)
+            o[name] = t
+    on.call(gdn_cache_plan, lens.data_ptr(), added.data_ptr(), block_table.data_ptr(), _some(free_list),
+            free_head.data_ptr(), o["cu_seqlens"].data_ptr(), _some(o["slots"]), _some(o["positions"]),
+            o["lens_out"].data_ptr(), o["free_head_out"].data_ptr(), o["status"].data_ptr(), N, max_blocks,
+            free_list.numel(), rows, int(page))
+    return CachePlan(o["cu_seqlens"], o["slots"], o["positions"], o["lens_out"], o["free_head_out"], o["status"])
+
+
+def _some(t):
+    return t.data_ptr() if t.numel() else None
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, d, dev):
+    if k_cache.dim() != 4 or k_cache.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("k_cache must be float8_e4m3fn (or its bytes, uint8) [num_pages, Hk, page, d]")
+    P, Hk, page, dc = k_cache.shape
+    if dc != d:
+        raise ValueError(f"k_cache has head size {dc}, expected {d}")
+    _need(k_cache, "k_cache", None, None, dev)
+    _need(v_cache, "v_cache", k_cache.dtype, (P, Hk, page, d), dev)
+    _need(k_scale, "k_scale", torch.float32, (P, Hk), dev)
+    _need(v_scale, "v_scale", torch.float32, (P, Hk), dev)
+    return P, Hk, page
+
+
+def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """Write new keys and values k, v [rows, Hk, d] into the paged e4m3 cache [num_pages, Hk, page, d] and
+    its scales [num_pages, Hk], in place, at ``slots`` (int32 [rows], as ``cache_plan`` gives them; -1: a
+    row without a token)."""
+    if k.dim() != 3:
+        raise ValueError("k must have 3 dimensions")
+    rows, Hk, d = k.shape
+    dt, dev, on = k.dtype, k.device, _On(k.device, stream)
+    if dt not in _DT:
+        raise ValueError(f"unsupported dtype {dt}")
+    P, Hc, page = _cache(k_cache, v_cache, k_scale, v_scale, d, dev)
+    _need(k, "k", dt, (rows, Hc, d))
+    _need(v, "v", dt, (rows, Hc, d), dev)
+    _need(slots, "slots", torch.int32, (rows,), dev)
+    on.call(gdn_cache_append, _some(k), _some(v), _some(slots), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), rows, Hk, d, page, P, _DT[dt])
+
+
+def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=None, out=None, workspace=None,
+                stream=None):
+    """One-token softmax attention q [N, Hq, d] over the paged e4m3 cache: request n attends to its first
+    lens[n] cached tokens through block_table [N, max_blocks]; scale defaults to 1 / sqrt(d).  Returns
+    out [N, Hq, d]; a request without tokens gets zeros."""
+    if q.dim() != 3:
+        raise ValueError("q must have 3 dimensions")
+    N, Hq, d = q.shape
+    dt, dev, on = q.dtype, q.device, _On(q.device, stream)
+    if dt not in _DT:
+        raise ValueError(f"unsupported dtype {dt}")
+    P, Hk, page = _cache(k_cache, v_cache, k_scale, v_scale, d, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have 2 dimensions")
+    max_blocks = block_table.shape[1]
+    _need(q, "q", dt, (N, Hq, d))
+    _need(block_table, "block_table", torch.int32, (N, max_blocks), dev)
+    _need(lens, "lens", torch.int32, (N,), dev)
+    out = on.new((N, Hq, d), dt) if out is None else out
+    _need(out, "out", dt, (N, Hq, d), dev)
+    need = on.query(gdn_attn_decode_workspace_bytes, N, Hq, Hk, d, page, max_blocks, _DT[dt])
+    ws, wbytes, _keep = on.scratch(workspace, need)
+    on.call(gdn_attn_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(), out.data_ptr(), N, Hq, Hk, d, page, P,
+            max_blocks, _DT[dt], _scale(scale, d), ws, wbytes)
     return out

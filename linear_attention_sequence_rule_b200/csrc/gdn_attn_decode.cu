@@ -1,0 +1,640 @@
+// gdn_attn_decode.cu -- one-token softmax attention over a paged e4m3 cache with one scale per
+// (page, head).
+//
+// Per (request, key head): s_j = scale q . (ks_j K8_j), out = sum_j softmax_j(s) vs_j V8_j over the
+// request's cached tokens, for the G query heads that share the key head.  HBM bounds it: 2 d bytes
+// per token and key head against 4 G d flops.  The cache is therefore read once for up to 16 query
+// heads: they are the M = 16 rows of warp-level MMAs (m16n8k16, fp16 operands, fp32 accumulators)
+// whose B operands are the cached bytes, converted to fp16 (exact) in registers.  At 2 d bytes per
+// token these MMAs leave the tensor pipe mostly idle, so the 128-row tcgen05 shape, which would pad
+// G rows to 128 and need the bytes converted through shared memory, has nothing to give here.
+//
+// Each warp runs alone: it takes every fourth 32-token tile of its CTA's range through its own ring
+// of TMA loads (K and V tiles of 32 rows, swizzled), keeps its own running maximum, sum and output
+// (online softmax), and the four warps join at the end.  A long context is split over CTAs whose
+// partial results a second kernel joins.
+//
+// The weights' frame: p_j = exp2(s_j + log2 vs_j - M), M = max_j (s_j + log2 vs_j), so that
+// p_j V8_j needs no further scale and p <= 1 fits fp16; the softmax sum takes p_j / vs_j.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "gdn_attn.h"
+#include "gdn_tmap.h"
+#include "sm100_ptx.cuh"
+#include "../../include/gdn.h"
+
+namespace gdn {
+
+using namespace sm100;
+
+__device__ int g_attn_decode_error = 0;
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int TT = 32;    // tokens per tile
+constexpr int NW = 4;     // warps per CTA
+constexpr int NSTG = 3;   // ring stages per warp
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// two e4m3 in the low half -> two fp16
+__device__ __forceinline__ uint32_t cvt_lo(uint32_t w)
+{
+    uint32_t r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t cvt_hi(uint32_t w)
+{
+    uint32_t r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// (page, head)-contiguous cache [pages][Hk][page][d] bytes: rows y.. of head z of page w
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int y, int z, int w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Tiles per split of a context of `len` tokens over at most `n` splits; those past its end are empty.
+__device__ __forceinline__ int split_tiles(int len, int n)
+{
+    const int tiles = (len + TT - 1) / TT;
+    return max(1, (tiles + n - 1) / n);
+}
+
+__device__ __forceinline__ int context_len(const int32_t *lens, int n, int max_blocks, int page)
+{
+    return (int)max(0LL, min((long long)lens[n], (long long)max_blocks * page));
+}
+
+// Partial results lie in the workspace as [request x query head][split][d + 4]: o, then m and l of the
+// frame above (two floats unused).
+
+template <bool F32> __device__ __forceinline__ void store_out(void *out, int64_t at, float4 x)
+{
+    if (F32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = x;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(out) + at) =
+            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+}
+
+template <int D> __host__ __device__ constexpr int stage_bytes() { return 2 * TT * D; }
+template <int D> __host__ __device__ constexpr int ring_bytes() { return NW * NSTG * stage_bytes<D>(); }
+// What a stage's tile needs besides its bytes: its pages' scales; a scale below 0 marks tokens that
+// are left out.
+struct TileInfo {
+    float ks0, ks1, vs0, vs1;  // tokens 0-15 and 16-31 of the tile
+};
+
+// behind the ring: the stages' info, barriers, then the warps' (m, l) for the join
+template <int D> __host__ __device__ constexpr int decode_smem()
+{
+    return 1024 + ring_bytes<D>() + NW * NSTG * ((int)sizeof(TileInfo) + 8) + NW * 16 * 8;
+}
+
+// F32: q as a sum of two fp16 in rows g and g + 8 (8 heads per tile), the weights likewise.
+template <int D, bool F32>
+__global__ void __launch_bounds__(NW * 32, 2)
+    attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const AttnDecodeArgs a, int splits, int mtiles)
+{
+    constexpr int MH = F32 ? 8 : 16;  // heads per tile
+    constexpr int KS = D / 16;        // k steps of the score product
+    constexpr int ND = D / 8;         // column tiles of the value product
+    constexpr int NG = D / 32;        // 4-byte words of a V row per thread
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    unsigned char *ring = sm + warp * NSTG * stage_bytes<D>();
+    TileInfo *info = reinterpret_cast<TileInfo *>(sm + ring_bytes<D>()) + warp * NSTG;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + ring_bytes<D>() + NW * NSTG * sizeof(TileInfo)) + warp * NSTG;
+    float2 *s_ml = reinterpret_cast<float2 *>(sm + ring_bytes<D>() + NW * NSTG * (sizeof(TileInfo) + 8));
+
+    int idx = blockIdx.x;
+    const int split = idx % splits;
+    idx /= splits;
+    const int mt = idx % mtiles;
+    idx /= mtiles;
+    const int hk = idx % a.Hk, n = idx / a.Hk;
+    const int G = a.Hq / a.Hk;
+    const int len = context_len(a.lens, n, a.max_blocks, a.page);
+    const int per = split_tiles(len, splits);
+    const int t0 = (int)min((long long)split * per * TT, (long long)len);
+    const int t1 = (int)min((long long)t0 + per * TT, (long long)len);
+    asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this grid's end
+    if (t0 >= t1 && split > 0) return;  // split 0 writes the zeros of an empty context
+
+    if (lane == 0) {
+        for (int i = 0; i < NSTG; ++i) mbar_init(&bar[i], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+
+    const int shift = __ffs(a.page) - 1;
+    const int tiles = (t1 - t0 + TT - 1) / TT;          // of this CTA; warp w takes tiles w, w + 4, ...
+    const int mine = tiles > warp ? (tiles - warp + NW - 1) / NW : 0;
+    const int32_t *table = a.table + (int64_t)n * a.max_blocks;
+    const bool small = a.page < TT;
+
+    // Page numbers and scales of 32 own tiles, one tile a lane (two pages where a page has 16
+    // tokens), with the next 32 fetched while these are worked on, so that the chain table -> scale
+    // is waited for once.
+    int pg0, pg1, npg0 = -1, npg1 = -1;
+    float ks0, ks1, vs0, vs1, nks0 = 0.f, nks1 = 0.f, nvs0 = 0.f, nvs1 = 0.f;
+    auto fetch_pages = [&](int i0, int &p0, int &p1) {
+        p0 = p1 = -1;
+        if (i0 + lane < mine) {
+            const int tok = t0 + (warp + NW * (i0 + lane)) * TT;
+            p0 = table[tok >> shift];
+            if (small) p1 = tok + 16 < t1 ? table[(tok >> shift) + 1] : -1;
+        }
+        if (p0 < 0 || p0 >= a.num_pages) p0 = -1;
+        if (p1 < 0 || p1 >= a.num_pages) p1 = -1;
+        if (!small) p1 = p0;
+    };
+    auto fetch_scales = [&](int p0, int p1, float &k0, float &k1, float &v0, float &v1) {
+        k0 = k1 = v0 = v1 = -1.f;
+        if (p0 >= 0) {
+            k0 = a.k_scale[(int64_t)p0 * a.Hk + hk];
+            v0 = fmaxf(a.v_scale[(int64_t)p0 * a.Hk + hk], 0x1p-60f);
+        }
+        if (!small) {
+            k1 = k0;
+            v1 = v0;
+        } else if (p1 >= 0) {
+            k1 = a.k_scale[(int64_t)p1 * a.Hk + hk];
+            v1 = fmaxf(a.v_scale[(int64_t)p1 * a.Hk + hk], 0x1p-60f);
+        }
+    };
+    // Loads of own tile i, in order.  Every tile brings 2 TT D bytes; page 0 stands in for a page
+    // out of range, whose tokens are left out.
+    auto load = [&](int i) {
+        const int at = i & 31;
+        if (at == 0 && i > 0) {
+            pg0 = npg0, pg1 = npg1;
+            ks0 = nks0, ks1 = nks1, vs0 = nvs0, vs1 = nvs1;
+        }
+        if (at == 8) fetch_pages(i - 8 + 32, npg0, npg1);
+        if (at == 20) fetch_scales(npg0, npg1, nks0, nks1, nvs0, nvs1);
+        const int p0 = max(__shfl_sync(0xffffffffu, pg0, at), 0), p1 = max(__shfl_sync(0xffffffffu, pg1, at), 0);
+        if (lane == at) info[i % NSTG] = TileInfo{ks0, ks1, vs0, vs1};
+        if (lane == 0) {
+            unsigned char *st = ring + (i % NSTG) * stage_bytes<D>();
+            uint64_t *b = &bar[i % NSTG];
+            mbar_arrive_expect_tx(b, stage_bytes<D>());
+            const int tok = t0 + (warp + NW * i) * TT;
+            const int y = tok & (a.page - 1);
+            tma_load_4d(st, &tmK, b, y, hk, p0);
+            tma_load_4d(st + TT * D, &tmV, b, y, hk, p0);
+            if (small) {
+                tma_load_4d(st + 16 * D, &tmK, b, 0, hk, p1);
+                tma_load_4d(st + TT * D + 16 * D, &tmV, b, 0, hk, p1);
+            }
+        }
+    };
+    fetch_pages(0, pg0, pg1);
+    fetch_scales(pg0, pg1, ks0, ks1, vs0, vs1);
+    int issued = 0;
+    for (; issued < NSTG && issued < mine; ++issued) load(issued);
+    __syncwarp();
+
+    // ---- q as A fragments; thread (g, c) holds rows g and g + 8 and, at k step ks, the four d values
+    // of its 16-byte chunks of a K row: chunk 2c + i (D = 128) or c (D = 64), word e, ks = 4 i + e ----
+    uint32_t qa[KS][4];
+    float unscale;  // score = accumulated x unscale x ks
+    {
+        const int h0 = mt * MH + g, h1 = F32 ? h0 : h0 + 8;
+        const bool on0 = h0 < G, on1 = h1 < G;
+        const int64_t r0 = ((int64_t)n * a.Hq + hk * G + h0) * D, r1 = ((int64_t)n * a.Hq + hk * G + h1) * D;
+        float x0[KS][4], x1[KS][4];
+        float mx = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const int d0 = 16 * (D == 128 ? 2 * c + (ks >> 2) : c) + 4 * (ks & 3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x0[ks][j] = x1[ks][j] = 0.f;
+            if (F32) {
+                const float *q = static_cast<const float *>(a.q);
+                if (on0) {
+                    const float4 w = *reinterpret_cast<const float4 *>(q + r0 + d0);
+                    x0[ks][0] = w.x, x0[ks][1] = w.y, x0[ks][2] = w.z, x0[ks][3] = w.w;
+                }
+            } else {
+                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
+                if (on0) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(q + r0 + d0);
+                    x0[ks][0] = __uint_as_float(w.x << 16), x0[ks][1] = __uint_as_float(w.x & 0xffff0000u);
+                    x0[ks][2] = __uint_as_float(w.y << 16), x0[ks][3] = __uint_as_float(w.y & 0xffff0000u);
+                }
+                if (on1) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(q + r1 + d0);
+                    x1[ks][0] = __uint_as_float(w.x << 16), x1[ks][1] = __uint_as_float(w.x & 0xffff0000u);
+                    x1[ks][2] = __uint_as_float(w.y << 16), x1[ks][3] = __uint_as_float(w.y & 0xffff0000u);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(x0[ks][j]), fabsf(x1[ks][j])));
+        }
+        // one power of two for the tile's rows brings the largest |q| into [256, 512): fp16 then
+        // holds values down to 2^-22 of it with full precision
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int e = mx > 0.f ? (int)(__float_as_uint(mx) >> 23) - 127 - 8 : 0;
+        const int ec = max(-126, min(e, 126));
+        const float down = __uint_as_float((uint32_t)(127 - ec) << 23);
+        unscale = __uint_as_float((uint32_t)(127 + ec) << 23) * a.scale * kLog2e;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x0[ks][j] *= down;
+                x1[ks][j] *= down;
+            }
+            if (F32) {  // row g + 8: what fp16 rounding of row g left over
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x1[ks][j] = x0[ks][j] - __half2float(__float2half_rn(x0[ks][j]));
+            }
+            qa[ks][0] = pack_half(x0[ks][0], x0[ks][1]);
+            qa[ks][1] = pack_half(x1[ks][0], x1[ks][1]);
+            qa[ks][2] = pack_half(x0[ks][2], x0[ks][3]);
+            qa[ks][3] = pack_half(x1[ks][2], x1[ks][3]);
+        }
+    }
+
+    float o[ND][4];
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // D = 64: a thread with odd c reads its token pairs in the other order (bank conflicts, below)
+    const uint32_t sel_lo = (D == 64 && (c & 1)) ? 0x1504u : 0x5140u, sel_hi = (D == 64 && (c & 1)) ? 0x3726u : 0x7362u;
+    const int odd = D == 64 ? (c & 1) : 0;
+    bool dead = false;
+    int done = 0;
+
+    for (int i = 0; i < mine; ++i, ++done) {
+        unsigned char *kt = ring + (i % NSTG) * stage_bytes<D>(), *vt = kt + TT * D;
+        if (!mbar_wait_bounded(&bar[i % NSTG], (i / NSTG) & 1, kWaitNs)) {
+            if (lane == 0) atomicOr(&g_attn_decode_error, 1);
+            dead = true;
+            break;
+        }
+        const int tok = t0 + (warp + NW * i) * TT;
+        const int live = min(TT, t1 - tok);
+        const TileInfo ti = info[i % NSTG];
+        const float kA = ti.ks0, ksB = ti.ks1, vA = ti.vs0, vsB = ti.vs1;
+        const bool onA = !(vA < 0.f), onB = !(vsB < 0.f);
+        // V rows that are not part of the context may hold any byte, NaN among them: zero them,
+        // since a weight of 0 times NaN is NaN
+        const bool partial = live < TT || !onA || !onB;
+        if (partial) {
+            for (int r = 0; r < TT; ++r)
+                if (r >= live || !(r < 16 ? onA : onB))
+                    for (int w = lane; w < D / 4; w += 32) reinterpret_cast<uint32_t *>(vt + r * D)[w] = 0u;
+            __syncwarp();
+        }
+        // ---- scores: 16 rows x 32 tokens ----
+        float s[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+            const int row = 8 * j + g;
+#pragma unroll
+            for (int i2 = 0; i2 < D / 64; ++i2) {
+                // the swizzle XORs the 16-byte chunk with the row (D = 128) or row pair (D = 64):
+                // the eight threads of a phase then read eight different chunk columns
+                const int ch = D == 128 ? ((2 * c + i2) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
+                const uint4 w = *reinterpret_cast<const uint4 *>(kt + row * D + ch * 16);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int ks = 4 * i2 + e;
+                    mma_f16(s[j], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], cvt_lo(ww[e]), cvt_hi(ww[e]));
+                }
+            }
+        }
+        // ---- softmax weights ----
+        const float fA = unscale * kA, fB = unscale * ksB;
+        const float lgA = onA ? log2f(vA) : 0.f, lgB = onB ? log2f(vsB) : 0.f;
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float f = j < 2 ? fA : fB, lg = j < 2 ? lgA : lgB;
+            const bool onj = j < 2 ? onA : onB;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bool on = onj && 8 * j + 2 * c + e < live;
+                if (F32) {
+                    const float x = s[j][e] + s[j][e + 2];
+                    s[j][e] = on ? fmaf(x, f, lg) : -INFINITY;
+                } else {
+                    s[j][e] = on ? fmaf(s[j][e], f, lg) : -INFINITY;
+                    s[j][e + 2] = on ? fmaf(s[j][e + 2], f, lg) : -INFINITY;
+                    mx1 = fmaxf(mx1, s[j][e + 2]);
+                }
+                mx0 = fmaxf(mx0, s[j][e]);
+            }
+        }
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
+            if (!F32) mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
+        }
+        const bool up = mx0 > m0 || (!F32 && mx1 > m1);
+        if (__any_sync(0xffffffffu, up)) {
+            const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+            const float f0 = n0 == -INFINITY ? 1.f : ex2_approx(m0 - n0);
+            const float f1 = F32 ? f0 : (n1 == -INFINITY ? 1.f : ex2_approx(m1 - n1));
+            m0 = n0;
+            m1 = n1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int x = 0; x < ND; ++x) {
+                o[x][0] *= f0;
+                o[x][1] *= f0;
+                o[x][2] *= f1;
+                o[x][3] *= f1;
+            }
+        }
+        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+        const float iA = onA ? 1.f / vA : 0.f, iB = onB ? 1.f / vsB : 0.f;
+        uint32_t pa[4][2];  // per 8-token column tile: rows g, g + 8
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float iv = j < 2 ? iA : iB;
+            const float x0 = ex2_approx(s[j][0] - b0), x1 = ex2_approx(s[j][1] - b0);
+            l0 = fmaf(x0 + x1, iv, l0);
+            pa[j][0] = pack_half(x0, x1);
+            if (F32) {
+                const __half2 hi = *reinterpret_cast<const __half2 *>(&pa[j][0]);
+                pa[j][1] = pack_half(x0 - __low2float(hi), x1 - __high2float(hi));
+            } else {
+                const float y0 = ex2_approx(s[j][2] - b1), y1 = ex2_approx(s[j][3] - b1);
+                l1 = fmaf(y0 + y1, iv, l1);
+                pa[j][1] = pack_half(y0, y1);
+            }
+        }
+        // ---- o += p V: k = 16 tokens a step; thread (g, c) reads words g + 8 x of the rows 2c, 2c + 1,
+        // 2c + 8, 2c + 9, column tile 4 x + b <-> d = 4 (g + 8 x) + b ----
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+#pragma unroll
+            for (int x = 0; x < NG; ++x) {
+                uint32_t w[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    // D = 64 packs two rows into 128 bytes; odd c swaps the rows of a pair so that a
+                    // phase's rows fall into both halves
+                    const int row = 16 * k2 + 2 * c + ((r & 1) ^ odd) + 8 * (r >> 1);
+                    const int ch = (g >> 2) + 2 * x;
+                    const int pos = D == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
+                    w[r] = *reinterpret_cast<const uint32_t *>(vt + row * D + pos * 16 + 4 * (g & 3));
+                }
+                // bytes of two tokens side by side: (token 2c, token 2c + 1) of each d
+                const uint32_t u0 = __byte_perm(w[0], w[1], sel_lo), u1 = __byte_perm(w[0], w[1], sel_hi);
+                const uint32_t z0 = __byte_perm(w[2], w[3], sel_lo), z1 = __byte_perm(w[2], w[3], sel_hi);
+                const uint32_t A0 = pa[2 * k2][0], A1 = pa[2 * k2][1], A2 = pa[2 * k2 + 1][0], A3 = pa[2 * k2 + 1][1];
+                mma_f16(o[4 * x + 0], A0, A1, A2, A3, cvt_lo(u0), cvt_lo(z0));
+                mma_f16(o[4 * x + 1], A0, A1, A2, A3, cvt_hi(u0), cvt_hi(z0));
+                mma_f16(o[4 * x + 2], A0, A1, A2, A3, cvt_lo(u1), cvt_lo(z1));
+                mma_f16(o[4 * x + 3], A0, A1, A2, A3, cvt_hi(u1), cvt_hi(z1));
+            }
+        }
+        if (partial) fence_proxy_async_smem();  // the zeros, before the stage's next bytes
+        __syncwarp();                           // every lane has read the stage
+        if (issued < mine) load(issued++);
+        __syncwarp();
+    }
+    if (dead)  // copies in flight end before the CTA does
+        for (int i = done; i < issued; ++i) mbar_wait_bounded(&bar[i % NSTG], (i / NSTG) & 1, kWaitNs);
+
+    // ---- the four warps join through shared memory (their rings are free now) ----
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+    if (F32) {
+#pragma unroll
+        for (int x = 0; x < ND; ++x) {
+            o[x][0] += o[x][2];
+            o[x][1] += o[x][3];
+        }
+    }
+    __syncthreads();
+    float *so = reinterpret_cast<float *>(sm) + warp * MH * D;
+    if (c == 0) {
+        s_ml[warp * 16 + g] = make_float2(m0, l0);
+        if (!F32) s_ml[warp * 16 + g + 8] = make_float2(m1, l1);
+    }
+#pragma unroll
+    for (int x = 0; x < NG; ++x) {
+        const int d0 = 4 * (2 * c + 8 * x);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            *reinterpret_cast<float4 *>(so + g * D + d0 + 4 * e) =
+                make_float4(o[4 * x][e], o[4 * x + 1][e], o[4 * x + 2][e], o[4 * x + 3][e]);
+            if (!F32)
+                *reinterpret_cast<float4 *>(so + (g + 8) * D + d0 + 4 * e) =
+                    make_float4(o[4 * x][2 + e], o[4 * x + 1][2 + e], o[4 * x + 2][2 + e], o[4 * x + 3][2 + e]);
+        }
+    }
+    __syncthreads();
+    const float *all = reinterpret_cast<const float *>(sm);
+    for (int i = tid; i < MH * (D / 4); i += NW * 32) {
+        const int r = i / (D / 4), d0 = 4 * (i % (D / 4)), h = mt * MH + r;
+        if (h >= G) continue;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w * 16 + r].x);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float2 ml = s_ml[w * 16 + r];
+            const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
+            const float4 y = *reinterpret_cast<const float4 *>(all + (w * MH + r) * D + d0);
+            L = fmaf(f, ml.y, L);
+            x.x = fmaf(f, y.x, x.x);
+            x.y = fmaf(f, y.y, x.y);
+            x.z = fmaf(f, y.z, x.z);
+            x.w = fmaf(f, y.w, x.w);
+        }
+        const int64_t row = (int64_t)n * a.Hq + hk * G + h;
+        if (splits > 1) {
+            float *ws = static_cast<float *>(a.workspace) + (row * splits + split) * (D + 4);
+            *reinterpret_cast<float4 *>(ws + d0) = x;
+            if (d0 == 0) *reinterpret_cast<float2 *>(ws + D) = make_float2(M, L);
+        } else {
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            store_out<F32>(a.out, row * D + d0, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+        }
+    }
+}
+
+// Joins the splits of one (request, query head): out = sum_s e_s o_s / sum_s e_s l_s, e_s =
+// exp2(m_s - max m).  One CTA a row; warp w takes splits w, w + 4, ...
+template <int D, bool F32>
+__global__ void __launch_bounds__(NW * 32) attn_decode_join(const AttnDecodeArgs a, int splits)
+{
+    constexpr int E = D / 32;  // elements of a row per lane
+    __shared__ float s_o[NW][D];
+    __shared__ float2 s_ml[NW];
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int len = context_len(a.lens, (int)(row / a.Hq), a.max_blocks, a.page);
+    const int tiles = (len + TT - 1) / TT, per = split_tiles(len, splits);
+    const int used = max(1, (tiles + per - 1) / per);
+    const float *ws = static_cast<const float *>(a.workspace) + row * splits * (D + 4);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float M = -INFINITY;
+    for (int s = lane; s < used; s += 32) M = fmaxf(M, ws[(int64_t)s * (D + 4) + D]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    float o[E], L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int s = warp; s < used; s += NW) {
+        const float *w = ws + (int64_t)s * (D + 4);
+        const float2 ml = *reinterpret_cast<const float2 *>(w + D);
+        const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
+        L = fmaf(f, ml.y, L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(f, w[lane + 32 * e], o[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = o[e];
+    if (lane == 0) s_ml[warp].y = L;
+    __syncthreads();
+    if (threadIdx.x < D / 4) {
+        const int d0 = 4 * threadIdx.x;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        L = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float4 y = *reinterpret_cast<const float4 *>(&s_o[w][d0]);
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            L += s_ml[w].y;
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        store_out<F32>(a.out, row * D + d0, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+    }
+}
+
+int sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 148;
+    }
+    return n;
+}
+
+int head_tiles(int G, int dtype) { return (G + (dtype == GDN_DTYPE_F32 ? 8 : 16) - 1) / (dtype == GDN_DTYPE_F32 ? 8 : 16); }
+
+// Splits of a context: enough CTAs for two per SM where there are few (request, key head) pairs, and
+// no split longer than 2048 tokens where contexts can be long (so that the longest contexts of a
+// ragged batch do not end the launch alone), but at least two tiles a warp.
+int split_count(int N, int Hk, int mtiles, int page, int max_blocks)
+{
+    const long tiles = ((long)max_blocks * page + TT - 1) / TT;
+    const long units = (long)N * Hk * mtiles;
+    long s = (2L * sm_count() + units - 1) / units;
+    const long by_len = (tiles + 63) / 64;
+    if (s < by_len) s = by_len < 8 ? by_len : (s > 8 ? s : 8);
+    const long most = tiles / (2 * NW);
+    if (s > most) s = most;
+    return (int)(s < 1 ? 1 : s);
+}
+
+bool cache_map(CUtensorMap *m, const void *base, int num_pages, int Hk, int page, int d)
+{
+    auto enc = tmap_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)Hk, (cuuint64_t)num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)d * page, (cuuint64_t)d * page * Hk};
+    const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)(page < TT ? page : TT), 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool F32> cudaError_t run_decode(const AttnDecodeArgs &a, cudaStream_t st)
+{
+    CUtensorMap mk, mv;
+    if (!cache_map(&mk, a.k_cache, a.num_pages, a.Hk, a.page, D) || !cache_map(&mv, a.v_cache, a.num_pages, a.Hk, a.page, D))
+        return cudaErrorInvalidValue;
+    const int mtiles = head_tiles(a.Hq / a.Hk, a.dtype);
+    const int splits = split_count(a.N, a.Hk, mtiles, a.page, a.max_blocks);
+    constexpr int smem = decode_smem<D>();
+    auto kern = attn_decode_kernel<D, F32>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)((long)a.N * a.Hk * mtiles * splits), NW * 32, smem, st>>>(mk, mv, a, splits, mtiles);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || splits == 1) return e;
+    // the join's CTAs may be set up while the last ones above run; they wait for all of them
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.N * a.Hq));
+    cfg.blockDim = dim3(NW * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_decode_join<D, F32>, a, splits);
+}
+
+}  // namespace
+
+size_t attn_decode_workspace_bytes(int N, int Hq, int Hk, int d, int page, int max_blocks, int dtype)
+{
+    const int splits = split_count(N, Hk, head_tiles(Hq / Hk, dtype), page, max_blocks);
+    return splits == 1 ? 0 : (size_t)N * Hq * splits * (d + 4) * sizeof(float);
+}
+
+cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t st)
+{
+    if (a.dtype == GDN_DTYPE_F32) return a.d == 128 ? run_decode<128, true>(a, st) : run_decode<64, true>(a, st);
+    return a.d == 128 ? run_decode<128, false>(a, st) : run_decode<64, false>(a, st);
+}
+
+int read_and_clear_attn_decode_error()
+{
+    int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attn_decode_error, sizeof(int)) != cudaSuccess) return -1;
+    if (v) cudaMemcpyToSymbol(g_attn_decode_error, &z, sizeof(int));
+    return v;
+}
+
+}  // namespace gdn
