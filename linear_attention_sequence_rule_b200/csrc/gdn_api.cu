@@ -329,9 +329,9 @@ int gdn_device_status(void *stream)
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "gdn_device_status");
     const int v1 = read_and_clear_tc_error(), v2 = read_and_clear_rowdecay_error();
-    const int v3 = read_and_clear_attn_decode_error();
-    if (v1 < 0 || v2 < 0 || v3 < 0) return fail(GDN_ERR_CUDA, "gdn_device_status: reading the device record failed");
-    const int v = v1 | v2 | v3;
+    const int v3 = read_and_clear_attn_decode_error(), v4 = read_and_clear_attn_fwd_error();
+    if (v1 < 0 || v2 < 0 || v3 < 0 || v4 < 0) return fail(GDN_ERR_CUDA, "gdn_device_status: reading the device record failed");
+    const int v = v1 | v2 | v3 | v4;
     if (v) return fail(GDN_ERR_TIMEOUT, "a device-side wait ran out (record 0x%x)", v);
     return GDN_OK;
 }

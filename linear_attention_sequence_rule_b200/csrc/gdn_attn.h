@@ -21,6 +21,11 @@ struct AttnArgs {
     float scale;
 };
 
+// bf16 on the tcgen05 tensor cores (gdn_attn_tc.cu); the device error record of its bounded waits,
+// read and cleared.
+cudaError_t launch_attn_fwd_tc(const AttnArgs &a, cudaStream_t stream);
+int read_and_clear_attn_fwd_error();
+
 // fp32 on CUDA cores (gdn_attn_simt.cu).
 cudaError_t launch_attn_fwd_simt(const AttnArgs &a, int dtype, cudaStream_t stream);
 cudaError_t launch_attn_bwd_simt(const AttnArgs &a, int dtype, cudaStream_t stream);

@@ -102,7 +102,8 @@ int gdn_attn_fwd(const void *q, const void *k, const void *v, void *out, float *
     AttnArgs a{};
     a.q = q, a.k = k, a.v = v, a.out = out, a.lse = lse;
     a.B = B, a.T = T, a.Hq = Hq, a.Hk = Hk, a.d = d, a.cu = cu_seqlens, a.scale = scale;
-    return launched(launch_attn_fwd_simt(a, dtype, static_cast<cudaStream_t>(stream)), fn);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return launched(dtype == GDN_DTYPE_BF16 ? launch_attn_fwd_tc(a, st) : launch_attn_fwd_simt(a, dtype, st), fn);
 }
 
 size_t gdn_attn_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d, int varlen, int dtype)

@@ -1,0 +1,308 @@
+// gdn_attn_tc.cu -- causal softmax attention over whole prompts on the tcgen05 tensor cores (bf16).
+//
+// Per (sequence, query head, 256 query rows): S = Q K^T, running maximum m and sum l of a softmax over
+// blocks of 128 keys, P = exp2(scale log2e S - m), O = O exp2(m_old - m) + P V, out = O / l,
+// lse = (m + log2 l) ln 2.
+//
+// One CTA holds two query tiles of 128 rows, which share every K and V tile that TMA brings (half the
+// L2 traffic of one tile).  Per tile, S (128 columns), O (D columns) and P (bf16, 64 columns; at
+// D = 128 over S's first columns, since S0, S1, O0, O1 fill the 512) sit in tensor memory.
+//   warps 0-3, 4-7   softmax of tile 0, 1: a thread holds a row
+//   warps 8, 9       one thread each issues the MMAs of tile 0, 1
+//   warp 10          loads; zeroes V rows behind the sequence's end
+// The tiles run apart: while one's softmax runs on the CUDA cores, the other's products fill the tensor
+// pipe.  The maximum is moved only when a row's new one passes it by 2^8 (weights up to 2^8 are as
+// exact in bf16), so that O is rarely rescaled.
+#include <math.h>
+
+#include "gdn_attn_tc.cuh"
+#include "gdn_internal.h"
+#include "../../include/gdn.h"
+
+namespace gdn {
+
+__device__ int g_attn_fwd_error = 0;
+
+namespace {
+
+using namespace attn;
+
+constexpr int NTH = 352;
+
+template <int D> struct FwdCfg {
+    static constexpr bool SEP = D == 64;      // P apart from S: the next S may come while P is formed
+    static constexpr int NS = D == 64 ? 4 : 2;  // K and V stages
+    static constexpr int TILE = BT * D * 2;
+    static constexpr int Q = 0, K = 2 * TILE, V = K + NS * TILE, BAR = V + NS * TILE;
+    // barriers
+    static constexpr int q_full = 0;                // [2]
+    static constexpr int k_full = 2;                // [NS]
+    static constexpr int k_empty = k_full + NS;     // [NS] both tiles' S products have read it
+    static constexpr int v_full = k_empty + NS;     // [NS]
+    static constexpr int v_empty = v_full + NS;     // [NS]
+    static constexpr int v_zeroed = v_empty + NS;   // [1]
+    static constexpr int s_full = v_zeroed + 1;     // [2] S of the block is there
+    static constexpr int s_free = s_full + 2;       // [2] S has been read (SEP)
+    static constexpr int p_half = s_free + 2;       // [2][2] columns 0-63, 64-127 of P are there
+    static constexpr int pv_done = p_half + 4;      // [2] O holds the block
+    static constexpr int drain = pv_done + 2;       // [2]
+    static constexpr int NBAR = drain + 2;
+    static constexpr int MISC = BAR + NBAR * 8;
+    static constexpr int TOTAL = 1024 + MISC + 16;
+    __host__ __device__ static constexpr uint32_t tS(int t) { return 128u * t; }
+    __host__ __device__ static constexpr uint32_t tO(int t) { return 256u + D * t; }
+    __host__ __device__ static constexpr uint32_t tP(int t) { return SEP ? 384u + 64u * t : tS(t); }
+};
+
+template <int D>
+__global__ void __launch_bounds__(NTH, 1)
+    attn_fwd_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
+                const int32_t *__restrict__ cu, int B, int T, int Hq, int Hk, float scale2)
+{
+    using C = FwdCfg<D>;
+    constexpr int NS = C::NS;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
+    int *abort_flag = reinterpret_cast<int *>(sm + C::MISC + 4);
+    const Waits w{abort_flag, &g_attn_fwd_error};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const AttnTile at = attn_tile(cu, B, T, 2 * BT, blockIdx.x / Hq);
+    if (at.seq < 0) return;
+    const int h = blockIdx.x % Hq, hk = h / (Hq / Hk);
+    const int q0 = at.block * 2 * BT, rows = at.len - q0;  // rows of this CTA's queries that exist
+    const int n0 = 2 * at.block + 1, n1 = rows > BT ? n0 + 1 : 0, nmax = n1 ? n1 : n0;  // key blocks per tile
+
+    if (tid == 0) {
+        for (int i = 0; i < C::NBAR; ++i) {
+            int n = 1;
+            if ((i >= C::k_empty && i < C::v_full) || (i >= C::v_empty && i < C::v_zeroed)) n = n1 ? 2 : 1;
+            if (i >= C::s_free && i < C::pv_done) n = BT;
+            mbar_init(&bar[i], n);
+        }
+        fence_mbar_init();
+        *abort_flag = 0;
+    }
+    if (warp == 10) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 10) {
+        // ---- loads ----
+        if (lane == 0) {
+            for (int t = 0; t < (n1 ? 2 : 1); ++t) {
+                mbar_arrive_expect_tx(&bar[C::q_full + t], C::TILE);
+                load_tile<D>(sm + C::Q + t * C::TILE, &tmQ, &bar[C::q_full + t], h, (int)at.t0 + q0 + t * BT);
+            }
+            for (int j = 0; j < nmax && !w.aborted(); ++j) {
+                const int s = j % NS;
+                if (j >= NS) w.wait(&bar[C::k_empty + s], j / NS - 1);
+                if (w.aborted()) break;
+                mbar_arrive_expect_tx(&bar[C::k_full + s], C::TILE);
+                load_tile<D>(sm + C::K + s * C::TILE, &tmK, &bar[C::k_full + s], hk, (int)at.t0 + j * BT);
+                if (j >= NS) w.wait(&bar[C::v_empty + s], j / NS - 1);
+                if (w.aborted()) break;
+                mbar_arrive_expect_tx(&bar[C::v_full + s], C::TILE);
+                load_tile<D>(sm + C::V + s * C::TILE, &tmV, &bar[C::v_full + s], hk, (int)at.t0 + j * BT);
+            }
+        }
+        __syncwarp();
+        const int last = at.len - (nmax - 1) * BT;
+        if (last < BT) {
+            const int s = (nmax - 1) % NS;
+            w.wait(&bar[C::v_full + s], (nmax - 1) / NS);
+            if (!w.aborted()) zero_rows<D>(sm + C::V + s * C::TILE, last, lane);
+            if (lane == 0) arrive(&bar[C::v_zeroed]);
+        }
+    } else if (warp >= 8) {
+        // ---- products of tile t ----
+        const int t = warp - 8, n = t ? n1 : n0;
+        if (lane == 0 && n > 0) {
+            const unsigned char *qt = sm + C::Q + t * C::TILE;
+            const uint32_t tS = tmem + C::tS(t), tO = tmem + C::tO(t), tP = tmem + C::tP(t);
+            auto scores = [&](int j) {
+                const int s = j % NS;
+                w.wait(&bar[C::k_full + s], j / NS);
+                if (w.aborted()) return;
+                tc_fence_after();
+                mma_nt<D>(tS, qt, sm + C::K + s * C::TILE);
+                mma_commit(&bar[C::s_full + t]);
+                mma_commit(&bar[C::k_empty + s]);
+            };
+            w.wait(&bar[C::q_full + t], 0);
+            scores(0);
+            for (int j = 0; j < n && !w.aborted(); ++j) {
+                const int s = j % NS;
+                if (C::SEP && j + 1 < n) {
+                    w.wait(&bar[C::s_free + t], j);
+                    scores(j + 1);
+                }
+                w.wait(&bar[C::v_full + s], j / NS);
+                if (j == nmax - 1 && at.len < nmax * BT) w.wait(&bar[C::v_zeroed], 0);
+                w.wait(&bar[C::p_half + 2 * t], j);
+                if (w.aborted()) break;
+                tc_fence_after();
+                mma_tn<D>(tO, tP, sm + C::V + s * C::TILE, 0, 4, j > 0);
+                w.wait(&bar[C::p_half + 2 * t + 1], j);
+                if (w.aborted()) break;
+                tc_fence_after();
+                mma_tn<D>(tO, tP, sm + C::V + s * C::TILE, 4, 8, true);
+                mma_commit(&bar[C::pv_done + t]);
+                mma_commit(&bar[C::v_empty + s]);
+                if (!C::SEP && j + 1 < n) {  // the next S overwrites P
+                    w.wait(&bar[C::pv_done + t], j);
+                    scores(j + 1);
+                }
+            }
+            if (t == 0 && n1) {  // tile 0 has no part in the last block
+                const int s = (nmax - 1) % NS;
+                w.wait(&bar[C::k_full + s], (nmax - 1) / NS);
+                arrive(&bar[C::k_empty + s]);
+                w.wait(&bar[C::v_full + s], (nmax - 1) / NS);
+                arrive(&bar[C::v_empty + s]);
+            }
+            if (w.aborted()) {  // products issued already end before the tensor memory is freed
+                mma_commit(&bar[C::drain + t]);
+                mbar_wait_bounded(&bar[C::drain + t], 0, 100000000ull);
+            }
+        }
+    } else {
+        // ---- softmax of tile t; thread = row ----
+        const int t = warp >> 2, n = t ? n1 : n0, wq = warp & 3, r = tid & (BT - 1);
+        const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+        const uint32_t tS = tmem + lanes + C::tS(t), tO = tmem + lanes + C::tO(t), tP = tmem + lanes + C::tP(t);
+        float m = -INFINITY, l = 0.f;  // m in units of S
+        for (int j = 0; j < n; ++j) {
+            float s[4][32];
+            w.wait(&bar[C::s_full + t], j);
+            if (w.aborted()) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tmem_ld32(tS + 32 * x, s[x]);
+            tmem_wait_ld();
+            if (C::SEP) {
+                tc_fence_before();
+                arrive(&bar[C::s_free + t]);
+            }
+            if (j == n - 1) {  // the diagonal block
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * x + i > r) s[x][i] = -INFINITY;
+            }
+            float mx[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                mx[x] = s[x][0];
+#pragma unroll
+                for (int i = 1; i < 32; ++i) mx[x] = fmaxf(mx[x], s[x][i]);
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (C::SEP && j > 0) {  // O is at rest, and the last P has been read
+                w.wait(&bar[C::pv_done + t], j - 1);
+                if (w.aborted()) break;
+                tc_fence_after();
+            }
+            const bool move = (top - m) * scale2 > 8.f;  // also from -inf
+            if (__any_sync(0xffffffffu, move)) {
+                const float to = move ? top : m;
+                const float f = move ? ex2_approx((m - to) * scale2) : 1.f;
+                m = to;
+                l *= f;
+                if (j > 0) {
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        float o[32];
+                        tmem_ld32(tO + 32 * x, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] *= f;
+                        tmem_st32(tO + 32 * x, o);
+                    }
+                }
+            }
+            const float ms = m == -INFINITY ? 0.f : m * scale2;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float p[32];  // 64 weights, two bf16 each
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int c = 64 * hf + 2 * i;
+                    const float a = ex2_approx(fmaf(s[c >> 5][c & 31], scale2, -ms));
+                    const float b = ex2_approx(fmaf(s[c >> 5][(c & 31) + 1], scale2, -ms));
+                    sum[i & 3] += a + b;
+                    p[i] = __uint_as_float(pack_bf16x2(a, b));
+                }
+                tmem_st32(tP + 32 * hf, p);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(&bar[C::p_half + 2 * t + hf]);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+        if (n > 0 && !w.aborted()) {
+            w.wait(&bar[C::pv_done + t], n - 1);
+            tc_fence_after();
+            if (!w.aborted()) {
+                const int64_t row0 = at.t0 + q0 + t * BT;
+                store_rows<D>(tO, 1.f / l, sm + C::Q + t * C::TILE, wq, lane, out + (row0 * Hq + h) * D, (int64_t)Hq * D,
+                              rows - t * BT);
+                if (lse && r < rows - t * BT) lse[(row0 + r) * Hq + h] = fmaf(m, scale2, log2f(l)) * kLn2;
+            }
+        }
+    }
+    if (w.aborted() && warp == 10 && lane == 0)  // copies in flight end before the CTA does
+        for (int i = C::q_full; i < C::v_zeroed; ++i)
+            if (i < C::k_empty || (i >= C::v_full && i < C::v_empty)) {
+                mbar_wait_bounded(&bar[i], 0, 1000000ull);
+                mbar_wait_bounded(&bar[i], 1, 1000000ull);
+            }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 10) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D> cudaError_t run_fwd(const AttnArgs &a, cudaStream_t st)
+{
+    using C = FwdCfg<D>;
+    const int64_t tokens = a.cu ? (int64_t)a.T : (int64_t)a.B * a.T;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, a.q, tokens, a.Hq, D) || !make_map(&mk, a.k, tokens, a.Hk, D) || !make_map(&mv, a.v, tokens, a.Hk, D))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(attn_fwd_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
+    if (e != cudaSuccess) return e;
+    const long tiles = attn_tiles(a.cu, a.B, a.T, 2 * BT);
+    attn_fwd_tc<D><<<(unsigned)(tiles * a.Hq), NTH, C::TOTAL, st>>>(mq, mk, mv, static_cast<__nv_bfloat16 *>(a.out), a.lse,
+                                                                   a.cu, a.B, a.T, a.Hq, a.Hk, a.scale * kLog2e);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_fwd_tc(const AttnArgs &a, cudaStream_t st)
+{
+    return a.d == 128 ? run_fwd<128>(a, st) : run_fwd<64>(a, st);
+}
+
+int read_and_clear_attn_fwd_error()
+{
+    int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attn_fwd_error, sizeof(int)) != cudaSuccess) return -1;
+    if (v) cudaMemcpyToSymbol(g_attn_fwd_error, &z, sizeof(int));
+    return v;
+}
+
+}  // namespace gdn

@@ -1,0 +1,140 @@
+// gdn_attn_tc.cuh -- what the tensor-core attention kernels (bf16) share: bounded waits, tile loads,
+// the MMA loops over a 128-row tile, and the exchange between TMEM rows and memory.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "gdn_attn.h"
+#include "gdn_attn_tile.cuh"
+#include "gdn_tmap.h"
+#include "sm100_ptx.cuh"
+
+namespace gdn {
+namespace attn {
+
+using namespace sm100;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int BT = 128;               // rows of every tile (queries or keys)
+constexpr int kSub = BT * 128;        // bytes of a 64-column sub-tile: 128 rows of 128 bytes, swizzled
+
+// Barriers with bounded waits: a wait that runs out records it and raises the CTA's abort flag, after
+// which no wait waits and no role issues work.
+struct Waits {
+    int *abort, *error;
+    __device__ __noinline__ void slow(uint64_t *b, uint32_t parity) const
+    {
+        if (!mbar_wait_bounded(b, parity, kWaitNs)) {
+            atomicOr(error, 1);
+            *(volatile int *)abort = 1;
+        }
+    }
+    __device__ __forceinline__ void wait(uint64_t *b, int phase) const
+    {
+        if (*(volatile int *)abort) return;
+        if (mbar_try_wait(b, phase & 1)) return;
+        slow(b, phase & 1);
+    }
+    __device__ __forceinline__ bool aborted() const { return *(volatile int *)abort != 0; }
+};
+
+__device__ __forceinline__ void arrive(uint64_t *b)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+
+// 128 rows of one head from token `row` on: D / 64 sub-tiles
+template <int D>
+__device__ __forceinline__ void load_tile(unsigned char *dst, const CUtensorMap *m, uint64_t *bar, int head, int row)
+{
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * kSub, m, bar, 64 * x, head, row);
+}
+
+// Zero rows n .. 127 of a tile (one warp): rows behind the sequence's end belong to a neighbour, and a
+// weight of 0 times a NaN there would be NaN.
+template <int D> __device__ __forceinline__ void zero_rows(unsigned char *tile, int n, int lane)
+{
+    for (int i = lane; i < (BT - n) * 8; i += 32)
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+            *reinterpret_cast<uint4 *>(tile + x * kSub + n * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// D[128 x 128] = A B^T over the head size: both tiles K-major in shared memory
+template <int D> __device__ __forceinline__ void mma_nt(uint32_t d, const unsigned char *a, const unsigned char *b)
+{
+    constexpr uint32_t id = idesc_bf16(BT, BT, 0, 0);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * kSub + (kk & 3) * 32;
+        mma_bf16(d, sdesc_sw128(smem_u32(a) + o, 16, 1024), sdesc_sw128(smem_u32(b) + o, 16, 1024), id, kk > 0);
+    }
+}
+
+// D[128 x D] (+)= A B: A (128 x 128, bf16) in tensor memory, B's rows (the 128 of the sum) in shared
+// memory, read MN-major; k steps k0 .. k1 - 1 of 16
+template <int D>
+__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, const unsigned char *b, int k0, int k1, bool accumulate)
+{
+    constexpr uint32_t id = idesc_bf16(BT, D, 0, 1);
+#pragma unroll
+    for (int kk = k0; kk < k1; ++kk)
+        mma_bf16_ta(d, a + 8 * kk, sdesc_sw128(smem_u32(b) + kk * 2048, kSub, 1024), id, accumulate || kk > k0);
+}
+
+// 32 fp32 accumulator rows (thread = row of its warp's 32; columns of `acc` at tensor memory address t)
+// scaled and written as bf16 rows: through the warp's own rows of `buf` (D * 2 bytes a row, 16-byte
+// units XORed with the row), then in whole rows to g + row * ld for rows below n.
+template <int D>
+__device__ __forceinline__ void store_rows(uint32_t t, float f, unsigned char *buf, int warp, int lane, __nv_bfloat16 *g,
+                                           int64_t ld, int n)
+{
+    constexpr int UN = D / 8;  // 16-byte units a row
+    const int r = 32 * warp + lane;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) {
+        float o[32];
+        tmem_ld32(t + 32 * x, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint4 w;
+            w.x = pack_bf16x2(o[8 * u] * f, o[8 * u + 1] * f);
+            w.y = pack_bf16x2(o[8 * u + 2] * f, o[8 * u + 3] * f);
+            w.z = pack_bf16x2(o[8 * u + 4] * f, o[8 * u + 5] * f);
+            w.w = pack_bf16x2(o[8 * u + 6] * f, o[8 * u + 7] * f);
+            *reinterpret_cast<uint4 *>(buf + r * (2 * D) + (((4 * x + u) ^ (r & 7)) << 4)) = w;
+        }
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int i = lane; i < 32 * UN; i += 32) {
+        const int rr = 32 * warp + i / UN, u = i % UN;
+        if (rr < n)
+            *reinterpret_cast<uint4 *>(g + (int64_t)rr * ld + 8 * u) =
+                *reinterpret_cast<const uint4 *>(buf + rr * (2 * D) + ((u ^ (rr & 7)) << 4));
+    }
+    __syncwarp();
+}
+
+// 3-D view [tokens][heads][d] of a bf16 tensor; box = 64 features x 1 head x 128 tokens, 128-byte swizzle
+inline bool make_map(CUtensorMap *m, const void *base, int64_t tokens, int heads, int d)
+{
+    auto enc = tmap_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    const cuuint32_t box[3] = {64, 1, BT};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace attn
+}  // namespace gdn

@@ -12,17 +12,17 @@ struct AttnTile {
     int64_t t0;  // the sequence's first token
 };
 
-// Tile `index` of a launch over blocks of `rows` tokens, sequence by sequence, each from its last
-// block to its first (under the causal mask the last query block has the most work).  Dense calls
-// have B ceil(T / rows) tiles; a packed launch has at most T / rows + B, and the tiles past the last
-// one are empty.  Called by whole warps; 32 sequences are looked at at a time.
+// Tile `index` of a launch over blocks of `rows` tokens, from last blocks to first ones (under the
+// causal mask the last query block has the most work): dense calls (B ceil(T / rows) tiles) block by
+// block over all sequences, packed ones (at most T / rows + B tiles; those past the last one are
+// empty) sequence by sequence.  Called by whole warps; 32 sequences are looked at at a time.
 __device__ __forceinline__ AttnTile attn_tile(const int32_t *__restrict__ cu, int B, int T, int rows, int index)
 {
     AttnTile r;
     if (!cu) {
         const int n = (T + rows - 1) / rows;
-        r.seq = index / n;
-        r.block = n - 1 - index % n;
+        r.seq = index % B;
+        r.block = n - 1 - index / B;
         r.len = T;
         r.t0 = (int64_t)r.seq * T;
         return r;
