@@ -27,7 +27,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int NTH = 352;
+constexpr int NTH = 384;
 
 template <int D> struct FwdCfg {
     static constexpr bool SEP = D == 64;      // P apart from S: the next S may come while P is formed
@@ -95,7 +95,10 @@ __global__ void __launch_bounds__(NTH, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 10) {
+    // registers: 384 x 168 = 64512 at launch; 128 x 48 + 256 x 224 = 63488 after the two roles' changes
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 10) {
         // ---- loads ----
         if (lane == 0) {
             for (int t = 0; t < (n1 ? 2 : 1); ++t) {
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(NTH, 1)
             if (!w.aborted()) zero_rows<D>(sm + C::V + s * C::TILE, last, lane);
             if (lane == 0) arrive(&bar[C::v_zeroed]);
         }
-    } else if (warp >= 8) {
+    } else if (warp < 10) {
         // ---- products of tile t ----
         const int t = warp - 8, n = t ? n1 : n0;
         if (lane == 0 && n > 0) {
@@ -174,7 +177,9 @@ __global__ void __launch_bounds__(NTH, 1)
                 mbar_wait_bounded(&bar[C::drain + t], 0, 100000000ull);
             }
         }
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ---- softmax of tile t; thread = row ----
         const int t = warp >> 2, n = t ? n1 : n0, wq = warp & 3, r = tid & (BT - 1);
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
@@ -202,9 +207,9 @@ __global__ void __launch_bounds__(NTH, 1)
             float mx[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                mx[x] = s[x][0];
+                mx[x] = fmaxf(s[x][0], s[x][1]);
 #pragma unroll
-                for (int i = 1; i < 32; ++i) mx[x] = fmaxf(mx[x], s[x][i]);
+                for (int i = 2; i < 32; i += 2) mx[x] = max3(mx[x], s[x][i], s[x][i + 1]);
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             if (C::SEP && j > 0) {  // O is at rest, and the last P has been read
@@ -231,16 +236,19 @@ __global__ void __launch_bounds__(NTH, 1)
                 }
             }
             const float ms = m == -INFINITY ? 0.f : m * scale2;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t sc2 = pack2(scale2, scale2), ms2 = pack2(-ms, -ms);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 float p[32];  // 64 weights, two bf16 each
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int c = 64 * hf + 2 * i;
-                    const float a = ex2_approx(fmaf(s[c >> 5][c & 31], scale2, -ms));
-                    const float b = ex2_approx(fmaf(s[c >> 5][(c & 31) + 1], scale2, -ms));
-                    sum[i & 3] += a + b;
+                    float a, b;
+                    unpack2(fma2(pack2(s[c >> 5][c & 31], s[c >> 5][(c & 31) + 1]), sc2, ms2), a, b);
+                    a = ex2_approx(a);
+                    b = ex2_approx(b);
+                    sum[i & 1] = add2(sum[i & 1], pack2(a, b));
                     p[i] = __uint_as_float(pack_bf16x2(a, b));
                 }
                 tmem_st32(tP + 32 * hf, p);
@@ -248,7 +256,9 @@ __global__ void __launch_bounds__(NTH, 1)
                 tc_fence_before();
                 arrive(&bar[C::p_half + 2 * t + hf]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            float a, b;
+            unpack2(add2(sum[0], sum[1]), a, b);
+            l += a + b;
         }
         if (n > 0 && !w.aborted()) {
             w.wait(&bar[C::pv_done + t], n - 1);
