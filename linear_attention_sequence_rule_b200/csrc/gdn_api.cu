@@ -330,8 +330,9 @@ int gdn_device_status(void *stream)
     if (e != cudaSuccess) return cuda_fail(e, "gdn_device_status");
     const int v1 = read_and_clear_tc_error(), v2 = read_and_clear_rowdecay_error();
     const int v3 = read_and_clear_attn_decode_error(), v4 = read_and_clear_attn_fwd_error();
-    if (v1 < 0 || v2 < 0 || v3 < 0 || v4 < 0) return fail(GDN_ERR_CUDA, "gdn_device_status: reading the device record failed");
-    const int v = v1 | v2 | v3 | v4;
+    const int v5 = read_and_clear_attn_bwd_error();
+    if (v1 < 0 || v2 < 0 || v3 < 0 || v4 < 0 || v5 < 0) return fail(GDN_ERR_CUDA, "gdn_device_status: reading the device record failed");
+    const int v = v1 | v2 | v3 | v4 | v5;
     if (v) return fail(GDN_ERR_TIMEOUT, "a device-side wait ran out (record 0x%x)", v);
     return GDN_OK;
 }

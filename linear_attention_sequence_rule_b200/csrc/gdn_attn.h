@@ -21,14 +21,16 @@ struct AttnArgs {
     float scale;
 };
 
-// bf16 on the tcgen05 tensor cores (gdn_attn_tc.cu); the device error record of its bounded waits,
-// read and cleared.
+// bf16 on the tcgen05 tensor cores (gdn_attn_tc.cu, gdn_attn_tc_bwd.cu); the device error records of
+// their bounded waits, read and cleared.
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_attn_bwd_tc(const AttnArgs &a, cudaStream_t stream);
 int read_and_clear_attn_fwd_error();
+int read_and_clear_attn_bwd_error();
 
 // fp32 on CUDA cores (gdn_attn_simt.cu).
-cudaError_t launch_attn_fwd_simt(const AttnArgs &a, int dtype, cudaStream_t stream);
-cudaError_t launch_attn_bwd_simt(const AttnArgs &a, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_attn_bwd_simt(const AttnArgs &a, cudaStream_t stream);
 
 struct CachePlanArgs {
     const int32_t *lens, *added;

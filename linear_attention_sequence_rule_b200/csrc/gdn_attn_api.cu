@@ -103,14 +103,15 @@ int gdn_attn_fwd(const void *q, const void *k, const void *v, void *out, float *
     a.q = q, a.k = k, a.v = v, a.out = out, a.lse = lse;
     a.B = B, a.T = T, a.Hq = Hq, a.Hk = Hk, a.d = d, a.cu = cu_seqlens, a.scale = scale;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return launched(dtype == GDN_DTYPE_BF16 ? launch_attn_fwd_tc(a, st) : launch_attn_fwd_simt(a, dtype, st), fn);
+    return launched(dtype == GDN_DTYPE_BF16 ? launch_attn_fwd_tc(a, st) : launch_attn_fwd_simt(a, st), fn);
 }
 
 size_t gdn_attn_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d, int varlen, int dtype)
 {
     if (check_prompt("gdn_attn_bwd", B, T, Hq, Hk, d, varlen, dtype) != GDN_OK) return (size_t)-1;
+    // D of every (token, query head); bf16: -lse log2 e too
     const size_t rows = (varlen ? (size_t)T : (size_t)B * T) * Hq;
-    return (rows * sizeof(float) + 255) & ~(size_t)255;
+    return (rows * (dtype == GDN_DTYPE_BF16 ? 2 : 1) * sizeof(float) + 255) & ~(size_t)255;
 }
 
 int gdn_attn_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse, const void *dout,
@@ -133,7 +134,8 @@ int gdn_attn_bwd(const void *q, const void *k, const void *v, const void *out, c
     a.q = q, a.k = k, a.v = v, a.out = const_cast<void *>(out), a.lse = const_cast<float *>(lse), a.dout = dout;
     a.dq = dq, a.dk = dk, a.dv = dv, a.workspace = workspace;
     a.B = B, a.T = T, a.Hq = Hq, a.Hk = Hk, a.d = d, a.cu = cu_seqlens, a.scale = scale;
-    return launched(launch_attn_bwd_simt(a, dtype, static_cast<cudaStream_t>(stream)), fn);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return launched(dtype == GDN_DTYPE_BF16 ? launch_attn_bwd_tc(a, st) : launch_attn_bwd_simt(a, st), fn);
 }
 
 int gdn_cache_plan(const int32_t *lens, const int32_t *added, int32_t *block_table, const int32_t *free_list,

@@ -13,13 +13,11 @@
 // rows hit 8 different bank groups).  256 threads as 16 x 16; a thread holds RPT rows (ty RPT + i)
 // and, in products over the head size, columns tx + 16 j; in products with D columns, the float4
 // groups tx + 16 g.
-#include <cuda_bf16.h>
 #include <math.h>
 
 #include "gdn_attn.h"
 #include "gdn_attn_tile.cuh"
 #include "sm100_ptx.cuh"
-#include "../../include/gdn.h"
 
 namespace gdn {
 
@@ -31,24 +29,13 @@ constexpr int BN = 64;       // keys per block
 constexpr int LDP = BN + 4;  // row stride of a score tile
 constexpr int NT = 256;
 
-template <typename T> __device__ __forceinline__ float4 load4(const T *p);
-template <> __device__ __forceinline__ float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p)
-{
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xffff0000u));
-}
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x)
-{
-    *reinterpret_cast<uint2 *>(p) = make_uint2(sm100::pack_bf16x2(x.x, x.y), sm100::pack_bf16x2(x.z, x.w));
-}
 
 // ROWS rows of one head, from row r0 on, into shared memory; rows past `len` are zero.  `g` is the
 // head's row 0 of the sequence, `ld` the elements between tokens.
-template <int ROWS, int D, typename T>
-__device__ __forceinline__ void load_tile(float *s, const T *g, int64_t ld, int r0, int len)
+template <int ROWS, int D>
+__device__ __forceinline__ void load_tile(float *s, const float *g, int64_t ld, int r0, int len)
 {
     constexpr int C = D / 4;
 #pragma unroll 4
@@ -147,14 +134,14 @@ __device__ __forceinline__ float row_sum16(float x)
 // ---- forward -------------------------------------------------------------------------------------
 
 // BM = 16 RPT query rows.
-template <typename T, int D, int RPT> constexpr int fwd_smem()
+template <int D, int RPT> constexpr int fwd_smem()
 {
     return ((16 * RPT + 2 * BN) * (D + 4) + 16 * RPT * LDP) * 4;
 }
 
-template <typename T, int D, int RPT>
-__global__ void __launch_bounds__(NT) attn_fwd_simt(const T *__restrict__ q, const T *__restrict__ k,
-                                                    const T *__restrict__ v, T *__restrict__ out,
+template <int D, int RPT>
+__global__ void __launch_bounds__(NT) attn_fwd_simt(const float *__restrict__ q, const float *__restrict__ k,
+                                                    const float *__restrict__ v, float *__restrict__ out,
                                                     float *__restrict__ lse, const int32_t *__restrict__ cu, int B,
                                                     int Tn, int Hq, int Hk, float scale2)
 {
@@ -167,7 +154,7 @@ __global__ void __launch_bounds__(NT) attn_fwd_simt(const T *__restrict__ q, con
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, ra = ty * RPT;
     const int q0 = t.block * BM;
     const int64_t ldq = (int64_t)Hq * D, ldk = (int64_t)Hk * D;
-    const T *kg = k + t.t0 * ldk + (int64_t)hk * D, *vg = v + t.t0 * ldk + (int64_t)hk * D;
+    const float *kg = k + t.t0 * ldk + (int64_t)hk * D, *vg = v + t.t0 * ldk + (int64_t)hk * D;
     load_tile<BM, D>(Qs, q + t.t0 * ldq + (int64_t)h * D, ldq, q0, t.len);
     float m[RPT], l[RPT];
     float4 o[RPT][D / 64];
@@ -223,7 +210,7 @@ __global__ void __launch_bounds__(NT) attn_fwd_simt(const T *__restrict__ q, con
         const float ls = row_sum16(l[i]);
         if (row >= t.len) continue;
         const float inv = 1.f / ls;
-        T *og = out + (t.t0 + row) * ldq + (int64_t)h * D;
+        float *og = out + (t.t0 + row) * ldq + (int64_t)h * D;
 #pragma unroll
         for (int g = 0; g < D / 64; ++g)
             store4(og + 4 * (tx + 16 * g),
@@ -235,8 +222,8 @@ __global__ void __launch_bounds__(NT) attn_fwd_simt(const T *__restrict__ q, con
 // ---- backward ------------------------------------------------------------------------------------
 
 // D_i = dout_i . out_i, one warp per (token, head)
-template <typename T, int D>
-__global__ void __launch_bounds__(NT) attn_bwd_dot(const T *__restrict__ out, const T *__restrict__ dout,
+template <int D>
+__global__ void __launch_bounds__(NT) attn_bwd_dot(const float *__restrict__ out, const float *__restrict__ dout,
                                                    float *__restrict__ dot, int64_t rows,
                                                    const int32_t *__restrict__ cu, int B, int Hq)
 {
@@ -285,11 +272,11 @@ __device__ __forceinline__ void load_rowstats(float *ls, float *dt, const float 
     }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(NT) attn_bwd_dq_simt(const T *__restrict__ q, const T *__restrict__ k,
-                                                       const T *__restrict__ v, const T *__restrict__ dout,
+template <int D>
+__global__ void __launch_bounds__(NT) attn_bwd_dq_simt(const float *__restrict__ q, const float *__restrict__ k,
+                                                       const float *__restrict__ v, const float *__restrict__ dout,
                                                        const float *__restrict__ lse, const float *__restrict__ dot,
-                                                       T *__restrict__ dq, const int32_t *__restrict__ cu, int B,
+                                                       float *__restrict__ dq, const int32_t *__restrict__ cu, int B,
                                                        int Tn, int Hq, int Hk, float scale)
 {
     extern __shared__ float sm[];
@@ -329,11 +316,11 @@ __global__ void __launch_bounds__(NT) attn_bwd_dq_simt(const T *__restrict__ q, 
     }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(NT) attn_bwd_dkv_simt(const T *__restrict__ q, const T *__restrict__ k,
-                                                        const T *__restrict__ v, const T *__restrict__ dout,
+template <int D>
+__global__ void __launch_bounds__(NT) attn_bwd_dkv_simt(const float *__restrict__ q, const float *__restrict__ k,
+                                                        const float *__restrict__ v, const float *__restrict__ dout,
                                                         const float *__restrict__ lse, const float *__restrict__ dot,
-                                                        T *__restrict__ dk, T *__restrict__ dv,
+                                                        float *__restrict__ dk, float *__restrict__ dv,
                                                         const int32_t *__restrict__ cu, int B, int Tn, int Hq, int Hk,
                                                         float scale)
 {
@@ -384,53 +371,49 @@ __global__ void __launch_bounds__(NT) attn_bwd_dkv_simt(const T *__restrict__ q,
     }
 }
 
-template <typename T, int D, int RPT> cudaError_t run_fwd(const AttnArgs &a, cudaStream_t st)
+template <int D, int RPT> cudaError_t run_fwd(const AttnArgs &a, cudaStream_t st)
 {
-    auto kern = attn_fwd_simt<T, D, RPT>;
-    constexpr int smem = fwd_smem<T, D, RPT>();
+    auto kern = attn_fwd_simt<D, RPT>;
+    constexpr int smem = fwd_smem<D, RPT>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)attn_tiles(a.cu, a.B, a.T, 16 * RPT), a.Hq);
-    kern<<<grid, NT, smem, st>>>((const T *)a.q, (const T *)a.k, (const T *)a.v, (T *)a.out, a.lse, a.cu, a.B, a.T,
+    kern<<<grid, NT, smem, st>>>((const float *)a.q, (const float *)a.k, (const float *)a.v, (float *)a.out, a.lse, a.cu, a.B, a.T,
                                  a.Hq, a.Hk, a.scale * kLog2e);
     return cudaGetLastError();
 }
 
-template <typename T, int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t st)
+template <int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t st)
 {
     constexpr int smem = bwd_smem<D>();
-    cudaError_t e = cudaFuncSetAttribute(attn_bwd_dq_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(attn_bwd_dq_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attn_bwd_dkv_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(attn_bwd_dkv_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t rows = (a.cu ? (int64_t)a.T : (int64_t)a.B * a.T) * a.Hq;
     float *dot = static_cast<float *>(a.workspace);
-    attn_bwd_dot<T, D><<<(unsigned)((rows + NT / 32 - 1) / (NT / 32)), NT, 0, st>>>((const T *)a.out, (const T *)a.dout,
+    attn_bwd_dot<D><<<(unsigned)((rows + NT / 32 - 1) / (NT / 32)), NT, 0, st>>>((const float *)a.out, (const float *)a.dout,
                                                                                  dot, rows, a.cu, a.B, a.Hq);
     const unsigned tiles = (unsigned)attn_tiles(a.cu, a.B, a.T, 64);
-    attn_bwd_dq_simt<T, D><<<dim3(tiles, a.Hq), NT, smem, st>>>((const T *)a.q, (const T *)a.k, (const T *)a.v,
-                                                                (const T *)a.dout, a.lse, dot, (T *)a.dq, a.cu, a.B,
+    attn_bwd_dq_simt<D><<<dim3(tiles, a.Hq), NT, smem, st>>>((const float *)a.q, (const float *)a.k, (const float *)a.v,
+                                                                (const float *)a.dout, a.lse, dot, (float *)a.dq, a.cu, a.B,
                                                                 a.T, a.Hq, a.Hk, a.scale);
-    attn_bwd_dkv_simt<T, D><<<dim3(tiles, a.Hk), NT, smem, st>>>((const T *)a.q, (const T *)a.k, (const T *)a.v,
-                                                                 (const T *)a.dout, a.lse, dot, (T *)a.dk, (T *)a.dv,
+    attn_bwd_dkv_simt<D><<<dim3(tiles, a.Hk), NT, smem, st>>>((const float *)a.q, (const float *)a.k, (const float *)a.v,
+                                                                 (const float *)a.dout, a.lse, dot, (float *)a.dk, (float *)a.dv,
                                                                  a.cu, a.B, a.T, a.Hq, a.Hk, a.scale);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_fwd_simt(const AttnArgs &a, int dtype, cudaStream_t st)
+cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t st)
 {
-    if (dtype == GDN_DTYPE_BF16)
-        return a.d == 128 ? run_fwd<__nv_bfloat16, 128, 4>(a, st) : run_fwd<__nv_bfloat16, 64, 4>(a, st);
-    return a.d == 128 ? run_fwd<float, 128, 4>(a, st) : run_fwd<float, 64, 4>(a, st);
+    return a.d == 128 ? run_fwd<128, 4>(a, st) : run_fwd<64, 4>(a, st);
 }
 
-cudaError_t launch_attn_bwd_simt(const AttnArgs &a, int dtype, cudaStream_t st)
+cudaError_t launch_attn_bwd_simt(const AttnArgs &a, cudaStream_t st)
 {
-    if (dtype == GDN_DTYPE_BF16)
-        return a.d == 128 ? run_bwd<__nv_bfloat16, 128>(a, st) : run_bwd<__nv_bfloat16, 64>(a, st);
-    return a.d == 128 ? run_bwd<float, 128>(a, st) : run_bwd<float, 64>(a, st);
+    return a.d == 128 ? run_bwd<128>(a, st) : run_bwd<64>(a, st);
 }
 
 }  // namespace gdn

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(NTH, 1)
         if (last < BT) {
             const int s = (nmax - 1) % NS;
             w.wait(&bar[C::v_full + s], (nmax - 1) / NS);
-            if (!w.aborted()) zero_rows<D>(sm + C::V + s * C::TILE, last, lane);
+            if (!w.stopped()) zero_rows<D>(sm + C::V + s * C::TILE, last, lane);
             if (lane == 0) arrive(&bar[C::v_zeroed]);
         }
     } else if (warp < 10) {
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(NTH, 1)
         for (int j = 0; j < n; ++j) {
             float s[4][32];
             w.wait(&bar[C::s_full + t], j);
-            if (w.aborted()) break;
+            if (w.stopped()) break;
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < 4; ++x) tmem_ld32(tS + 32 * x, s[x]);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(NTH, 1)
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             if (C::SEP && j > 0) {  // O is at rest, and the last P has been read
                 w.wait(&bar[C::pv_done + t], j - 1);
-                if (w.aborted()) break;
+                if (w.stopped()) break;
                 tc_fence_after();
             }
             const bool move = (top - m) * scale2 > 8.f;  // also from -inf
@@ -260,10 +260,10 @@ __global__ void __launch_bounds__(NTH, 1)
             unpack2(add2(sum[0], sum[1]), a, b);
             l += a + b;
         }
-        if (n > 0 && !w.aborted()) {
+        if (n > 0 && !w.stopped()) {
             w.wait(&bar[C::pv_done + t], n - 1);
             tc_fence_after();
-            if (!w.aborted()) {
+            if (!w.stopped()) {
                 const int64_t row0 = at.t0 + q0 + t * BT;
                 store_rows<D>(tO, 1.f / l, sm + C::Q + t * C::TILE, wq, lane, out + (row0 * Hq + h) * D, (int64_t)Hq * D,
                               rows - t * BT);

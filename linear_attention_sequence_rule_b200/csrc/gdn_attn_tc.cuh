@@ -38,6 +38,8 @@ struct Waits {
         slow(b, phase & 1);
     }
     __device__ __forceinline__ bool aborted() const { return *(volatile int *)abort != 0; }
+    // the same for a whole warp, so that its lanes leave a loop together
+    __device__ __forceinline__ bool stopped() const { return __any_sync(0xffffffffu, aborted()); }
 };
 
 __device__ __forceinline__ void arrive(uint64_t *b)

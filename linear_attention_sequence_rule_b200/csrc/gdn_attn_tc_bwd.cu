@@ -1,0 +1,621 @@
+// gdn_attn_tc_bwd.cu -- gradients of causal softmax attention on the tcgen05 tensor cores (bf16).
+//
+//   P = exp(scale Q K^T - lse),  dP = dO V^T,  dS = P (dP - D),  D_i = dO_i . O_i
+//   dQ = scale dS K,   dK = scale dS^T Q,   dV = P^T dO
+//
+// Two launches.  The query side holds a block of 128 query rows and passes over its key blocks (S, dP
+// and dQ: three products a step); the key side holds a block of 128 keys and passes over the query
+// heads that share them and their query blocks (S^T, dP^T, dV, dK: four products a step).  S and dP
+// are formed twice (seven products where one kernel would need five), and in return every gradient is
+// summed in tensor memory by one CTA in one order: no atomics, no partial sums in HBM, a call repeats
+// bit for bit.
+//
+// D from the rounded result is off by 2^-9 |dO| |O|, which counts where few keys carry a row: a row
+// that sees one key has dS = 0, and what is left is that error.  The first kExactBlocks query
+// blocks of a sequence therefore form D as sum_j P_ij dP_ij in a pass of their own; behind them rows
+// average over more keys, and D is taken from out.  The query side writes D and -lse log2 e for
+// the key side, head by head ([Hq][tokens] each), into the workspace.
+//
+// In both kernels warps 0-7 work element by element (a thread has a row; two groups of 4 warps take
+// different 32-column chunks), one thread of warp 8 issues the products, warp 9 loads.  P and dS (bf16)
+// are written over the first half of the very S or dP columns they came from, which their own
+// thread has read.
+#include <math.h>
+
+#include "gdn_attn_tc.cuh"
+#include "gdn_internal.h"
+#include "../../include/gdn.h"
+
+namespace gdn {
+
+__device__ int g_attn_bwd_error = 0;
+
+namespace {
+
+using namespace attn;
+
+constexpr int NTH = 320;
+constexpr int NEL = 256;         // threads of the element-wise warps
+constexpr int kExactBlocks = 2;
+
+// D[128 x D] (+)= A B with A's chunks of 32 columns (16 of tensor memory) 32 apart: k steps k0 .. k1 - 1
+template <int D>
+__device__ __forceinline__ void mma_chunks(uint32_t d, uint32_t a, const unsigned char *b, int k0, int k1, bool accumulate)
+{
+    constexpr uint32_t id = idesc_bf16(BT, D, 0, 1);
+#pragma unroll
+    for (int kk = k0; kk < k1; ++kk)
+        mma_bf16_ta(d, a + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_sw128(smem_u32(b) + kk * 2048, kSub, 1024), id,
+                    accumulate || kk > k0);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void named_bar(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// After a wait ran out: copies in flight end before the CTA does.
+__device__ __forceinline__ void drain_loads(uint64_t *bar, int first, int count)
+{
+    for (int i = first; i < first + count; ++i) {
+        mbar_wait_bounded(&bar[i], 0, 1000000ull);
+        mbar_wait_bounded(&bar[i], 1, 1000000ull);
+    }
+}
+
+// ---- query side ------------------------------------------------------------------------------------
+
+template <int D> struct DqCfg {
+    static constexpr int NS = D == 64 ? 4 : 2;
+    static constexpr int TILE = BT * D * 2;
+    static constexpr int Q = 0, O = TILE, K = 2 * TILE, V = K + NS * TILE, RED = V + NS * TILE, BAR = RED + 2 * BT * 4;
+    static constexpr int q_full = 0;               // Q and dO
+    static constexpr int k_full = 1;               // [NS]
+    static constexpr int v_full = k_full + NS;     // [NS]
+    static constexpr int k_empty = v_full + NS;    // [NS]
+    static constexpr int v_empty = k_empty + NS;   // [NS]
+    static constexpr int zeroed = v_empty + NS;    // [NS] the stage has no row behind the end (ragged ends only)
+    static constexpr int s_full = zeroed + NS;     // [2]
+    static constexpr int dp_full = s_full + 2;
+    static constexpr int dp_free = dp_full + 1;    // dP has been read
+    static constexpr int ds_full = dp_free + 1;    // [2] dS is there (first pass: S has been read)
+    static constexpr int dq_done = ds_full + 2;    // [2] dS has been used
+    static constexpr int drain = dq_done + 2;
+    static constexpr int NBAR = drain + 1;
+    static constexpr int MISC = BAR + NBAR * 8;
+    static constexpr int TOTAL = 1024 + MISC + 16;
+    static constexpr uint32_t tS = 0, tP = 256, tQ = 384;  // S[2], dP, dQ
+};
+
+template <int D>
+__global__ void __launch_bounds__(NTH, 1)
+    attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                   const __nv_bfloat16 *__restrict__ out, const float *__restrict__ lse, __nv_bfloat16 *__restrict__ dq,
+                   float *__restrict__ nlse, float *__restrict__ ndot, const int32_t *__restrict__ cu, int B, int T,
+                   int Hq, int Hk, float scale, int64_t tokens)
+{
+    using C = DqCfg<D>;
+    constexpr int NS = C::NS;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
+    int *abort_flag = reinterpret_cast<int *>(sm + C::MISC + 4);
+    float *red = reinterpret_cast<float *>(sm + C::RED);
+    const Waits w{abort_flag, &g_attn_bwd_error};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const AttnTile at = attn_tile(cu, B, T, BT, blockIdx.x / Hq);
+    if (at.seq < 0) return;
+    const int h = blockIdx.x % Hq, hk = h / (Hq / Hk);
+    const int n = at.block + 1;                    // key blocks
+    const bool exact = at.block < kExactBlocks;
+    const int steps = exact ? 2 * n : n;           // the first n form D
+    const int rows = at.len - at.block * BT;       // that exist
+    const int64_t row0 = at.t0 + at.block * BT;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::NBAR; ++i)
+            mbar_init(&bar[i], i == C::dp_free || (i >= C::ds_full && i < C::dq_done) ? NEL : 1);
+        fence_mbar_init();
+        *abort_flag = 0;
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 9) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bar[C::q_full], 2 * C::TILE);
+            load_tile<D>(sm + C::Q, &tmQ, &bar[C::q_full], h, (int)row0);
+            load_tile<D>(sm + C::O, &tmO, &bar[C::q_full], h, (int)row0);
+        }
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % NS, j = i % n;
+            if (lane == 0) {
+                if (i >= NS) w.wait(&bar[C::k_empty + s], i / NS - 1);
+                if (!w.aborted()) {
+                    mbar_arrive_expect_tx(&bar[C::k_full + s], C::TILE);
+                    load_tile<D>(sm + C::K + s * C::TILE, &tmK, &bar[C::k_full + s], hk, (int)at.t0 + j * BT);
+                }
+                if (i >= NS) w.wait(&bar[C::v_empty + s], i / NS - 1);
+                if (!w.aborted()) {
+                    mbar_arrive_expect_tx(&bar[C::v_full + s], C::TILE);
+                    load_tile<D>(sm + C::V + s * C::TILE, &tmV, &bar[C::v_full + s], hk, (int)at.t0 + j * BT);
+                }
+            }
+            __syncwarp();
+            if (w.stopped()) break;
+            if (j == n - 1 && rows < BT) {
+                w.wait(&bar[C::k_full + s], i / NS);
+                w.wait(&bar[C::v_full + s], i / NS);
+                if (w.stopped()) break;
+                zero_rows<D>(sm + C::K + s * C::TILE, rows, lane);
+                zero_rows<D>(sm + C::V + s * C::TILE, rows, lane);
+            }
+            if (rows < BT && lane == 0) arrive(&bar[C::zeroed + s]);
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            auto arrived = [&](int first, int i) {  // step i's tile, and its zeros
+                w.wait(&bar[first + i % NS], i / NS);
+                if (rows < BT) w.wait(&bar[C::zeroed + i % NS], i / NS);
+            };
+            auto scores = [&](int i) {
+                arrived(C::k_full, i);
+                if (w.aborted()) return;
+                tc_fence_after();
+                mma_nt<D>(tmem + C::tS + 128 * (i & 1), sm + C::Q, sm + C::K + (i % NS) * C::TILE);
+                mma_commit(&bar[C::s_full + (i & 1)]);
+            };
+            auto dprobs = [&](int i) {
+                arrived(C::v_full, i);
+                if (w.aborted()) return;
+                tc_fence_after();
+                mma_nt<D>(tmem + C::tP, sm + C::O, sm + C::V + (i % NS) * C::TILE);
+                mma_commit(&bar[C::dp_full]);
+                mma_commit(&bar[C::v_empty + i % NS]);
+            };
+            w.wait(&bar[C::q_full], 0);
+            scores(0);
+            dprobs(0);
+            for (int i = 0; i < steps && !w.aborted(); ++i) {
+                if (i + 1 < steps) {
+                    if (i > 0) w.wait(&bar[C::dq_done + ((i + 1) & 1)], (i - 1) >> 1);
+                    scores(i + 1);
+                    w.wait(&bar[C::dp_free], i);
+                    dprobs(i + 1);
+                }
+                w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
+                if (w.aborted()) break;
+                tc_fence_after();
+                if (i >= steps - n)
+                    mma_chunks<D>(tmem + C::tQ, tmem + C::tS + 128 * (i & 1), sm + C::K + (i % NS) * C::TILE, 0, 8,
+                                  i > steps - n);
+                mma_commit(&bar[C::dq_done + (i & 1)]);
+                mma_commit(&bar[C::k_empty + i % NS]);
+            }
+            if (w.aborted()) {
+                mma_commit(&bar[C::drain]);
+                mbar_wait_bounded(&bar[C::drain], 0, 100000000ull);
+            }
+        }
+    } else {
+        const int g = warp >> 2, wq = warp & 3, r = tid & (BT - 1);
+        const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+        const bool live = r < rows;
+        const float nl = live ? -lse[(row0 + r) * Hq + h] * kLog2e : 0.f;
+        float nd = 0.f;
+        if (!exact) {  // D from out: this thread's half of the row
+            w.wait(&bar[C::q_full], 0);
+            if (live) {
+                const uint4 *o = reinterpret_cast<const uint4 *>(out + ((row0 + r) * Hq + h) * D) + g * (D / 16);
+#pragma unroll
+                for (int u = 0; u < D / 16; ++u) {
+                    const int x = g * (D / 16) + u;
+                    const uint4 a = o[u], b = *reinterpret_cast<const uint4 *>(sm + C::O + (x >> 3) * kSub + r * 128 +
+                                                                               (((x & 7) ^ (r & 7)) << 4));
+                    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        nd = fmaf(__uint_as_float(av[e] << 16), -__uint_as_float(bv[e] << 16), nd);
+                        nd = fmaf(__uint_as_float(av[e] & 0xffff0000u), -__uint_as_float(bv[e] & 0xffff0000u), nd);
+                    }
+                }
+            }
+        }
+        auto join = [&]() {  // the two halves of D; for the key side too
+            red[g * BT + r] = nd;
+            named_bar(1, NEL);
+            nd = red[r] + red[BT + r];
+            if (g == 0 && live) {
+                nlse[(int64_t)h * tokens + row0 + r] = nl;
+                ndot[(int64_t)h * tokens + row0 + r] = nd;
+            }
+        };
+        bool joined = !exact;
+        if (joined) join();
+        const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e), nl2 = pack2(nl, nl);
+        for (int i = 0; i < steps; ++i) {
+            if (!joined && i == n) {
+                join();
+                joined = true;
+            }
+            const uint64_t nd2 = pack2(nd, nd);
+            const uint32_t tS = tmem + lanes + C::tS + 128 * (i & 1) + 64 * g, tP = tmem + lanes + C::tP + 64 * g;
+            float s[2][32];
+            w.wait(&bar[C::s_full + (i & 1)], i >> 1);
+            if (w.stopped()) break;
+            tc_fence_after();
+            tmem_ld32(tS, s[0]);
+            tmem_ld32(tS + 32, s[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                    unpack2(fma2(pack2(s[q][x], s[q][x + 1]), sc2, nl2), s[q][x], s[q][x + 1]);
+                    s[q][x] = ex2_approx(s[q][x]);
+                    s[q][x + 1] = ex2_approx(s[q][x + 1]);
+                }
+            if (i % n == n - 1) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (64 * g + 32 * q + x > r) s[q][x] = 0.f;
+            }
+            float dp[2][32];
+            w.wait(&bar[C::dp_full], i);
+            if (w.stopped()) break;
+            tc_fence_after();
+            tmem_ld32(tP, dp[0]);
+            tmem_ld32(tP + 32, dp[1]);
+            tmem_wait_ld();
+            tc_fence_before();
+            arrive(&bar[C::dp_free]);
+            if (i < steps - n) {
+                uint64_t acc = 0;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2)
+                        acc = fma2(pack2(s[q][x], s[q][x + 1]), pack2(dp[q][x], dp[q][x + 1]), acc);
+                float a, b;
+                unpack2(acc, a, b);
+                nd -= a + b;
+            } else {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t ds[16];
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) {
+                        float a, b;
+                        unpack2(mul2(pack2(s[q][x], s[q][x + 1]), add2(pack2(dp[q][x], dp[q][x + 1]), nd2)), a, b);
+                        ds[x >> 1] = pack_bf16x2(a, b);
+                    }
+                    tmem_st16(tS + 32 * q, ds);
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            arrive(&bar[C::ds_full + (i & 1)]);
+        }
+        if (!joined) named_bar(1, NEL);  // left early: the other warps still come by
+        if (!w.stopped()) {
+            w.wait(&bar[C::dq_done + ((steps - 1) & 1)], (steps - 1) >> 1);
+            tc_fence_after();
+            if (!w.stopped() && g == 0)
+                store_rows<D>(tmem + lanes + C::tQ, scale, sm + C::Q, wq, lane, dq + (row0 * Hq + h) * D, (int64_t)Hq * D,
+                              rows);
+        }
+    }
+    if (w.aborted() && warp == 9 && lane == 0) drain_loads(bar, C::q_full, 1 + 2 * NS);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---- key side ----------------------------------------------------------------------------------------
+
+template <int D> struct DkvCfg {
+    static constexpr int NS = D == 64 ? 4 : 2;
+    static constexpr int TILE = BT * D * 2;
+    static constexpr int K = 0, V = TILE, Q = 2 * TILE, O = Q + NS * TILE, ST = O + NS * TILE, BAR = ST + NS * 2 * BT * 4;
+    static constexpr int kv_full = 0;
+    static constexpr int q_full = 1;               // [NS] Q, and -lse log2 e and -D of its rows
+    static constexpr int o_full = q_full + NS;     // [NS] dO
+    static constexpr int empty = o_full + NS;      // [NS] the stage has been used
+    static constexpr int zeroed = empty + NS;      // [NS] the stage has no row behind the end (ragged ends only)
+    static constexpr int s_full = zeroed + NS;
+    static constexpr int dp_full = s_full + 1;
+    static constexpr int p_half = dp_full + 1;     // [2] columns 0-63, 64-127 of P^T are there
+    static constexpr int ds_full = p_half + 2;
+    static constexpr int dv_done = ds_full + 1;    // P^T has been used
+    static constexpr int dk_done = dv_done + 1;    // dS^T has been used
+    static constexpr int drain = dk_done + 1;
+    static constexpr int NBAR = drain + 1;
+    static constexpr int MISC = BAR + NBAR * 8;
+    static constexpr int TOTAL = 1024 + MISC + 16;
+    static constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // S^T, dP^T, dV, dK
+};
+
+template <int D>
+__global__ void __launch_bounds__(NTH, 1)
+    attn_bwd_dkv_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                    const float *__restrict__ nlse, const float *__restrict__ ndot, __nv_bfloat16 *__restrict__ dk,
+                    __nv_bfloat16 *__restrict__ dv, const int32_t *__restrict__ cu, int B, int T, int Hq, int Hk,
+                    float scale, int64_t tokens)
+{
+    using C = DkvCfg<D>;
+    constexpr int NS = C::NS;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
+    int *abort_flag = reinterpret_cast<int *>(sm + C::MISC + 4);
+    const Waits w{abort_flag, &g_attn_bwd_error};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const AttnTile at = attn_tile(cu, B, T, BT, blockIdx.x / Hk);
+    if (at.seq < 0) return;
+    const int hk = blockIdx.x % Hk, G = Hq / Hk;
+    const int blocks = (at.len + BT - 1) / BT;
+    const int kb = blocks - 1 - at.block;          // the first key blocks see the most queries
+    const int n = blocks - kb;                     // query blocks per head
+    const int steps = G * n;
+    const int rows = at.len - kb * BT;             // keys that exist
+    const int tail = at.len - (blocks - 1) * BT;   // queries of the last block
+    const int64_t row0 = at.t0 + kb * BT;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::NBAR; ++i) {
+            int c = 1;
+            if (i >= C::q_full && i < C::o_full) c = 1 + 32;
+            if ((i >= C::p_half && i < C::ds_full) || i == C::ds_full) c = NEL;
+            mbar_init(&bar[i], c);
+        }
+        fence_mbar_init();
+        *abort_flag = 0;
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 9) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bar[C::kv_full], 2 * C::TILE);
+            load_tile<D>(sm + C::K, &tmK, &bar[C::kv_full], hk, (int)row0);
+            load_tile<D>(sm + C::V, &tmV, &bar[C::kv_full], hk, (int)row0);
+        }
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % NS, h = hk * G + i / n, qb = kb + i % n;
+            if (i >= NS) w.wait(&bar[C::empty + s], i / NS - 1);
+            if (w.stopped()) break;
+            const int64_t q0 = at.t0 + qb * BT;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar[C::q_full + s], C::TILE);
+                load_tile<D>(sm + C::Q + s * C::TILE, &tmQ, &bar[C::q_full + s], h, (int)q0);
+                mbar_arrive_expect_tx(&bar[C::o_full + s], C::TILE);
+                load_tile<D>(sm + C::O + s * C::TILE, &tmO, &bar[C::o_full + s], h, (int)q0);
+            }
+            // rows behind the end get 0, 0: a weight of 1 on a row of zeros
+            float *st = reinterpret_cast<float *>(sm + C::ST) + s * 2 * BT;
+            const int live = qb == blocks - 1 ? tail : BT;
+#pragma unroll
+            for (int x = lane; x < BT; x += 32) {
+                const int64_t o = (int64_t)h * tokens + q0 + min(x, live - 1);
+                cp_async_4(st + x, nlse + o, x < live ? 4u : 0u);
+                cp_async_4(st + BT + x, ndot + o, x < live ? 4u : 0u);
+            }
+            cp_async_mbar_arrive(&bar[C::q_full + s]);
+            if (qb == blocks - 1 && tail < BT) {
+                w.wait(&bar[C::q_full + s], i / NS);
+                w.wait(&bar[C::o_full + s], i / NS);
+                if (w.stopped()) break;
+                zero_rows<D>(sm + C::Q + s * C::TILE, tail, lane);
+                zero_rows<D>(sm + C::O + s * C::TILE, tail, lane);
+            }
+            if (tail < BT && lane == 0) arrive(&bar[C::zeroed + s]);
+            __syncwarp();
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            auto arrived = [&](int first, int i) {
+                w.wait(&bar[first + i % NS], i / NS);
+                if (tail < BT) w.wait(&bar[C::zeroed + i % NS], i / NS);
+            };
+            auto scores = [&](int i) {
+                arrived(C::q_full, i);
+                if (w.aborted()) return;
+                tc_fence_after();
+                mma_nt<D>(tmem + C::tS, sm + C::K, sm + C::Q + (i % NS) * C::TILE);
+                mma_commit(&bar[C::s_full]);
+            };
+            auto dprobs = [&](int i) {
+                arrived(C::o_full, i);
+                if (w.aborted()) return;
+                tc_fence_after();
+                mma_nt<D>(tmem + C::tP, sm + C::V, sm + C::O + (i % NS) * C::TILE);
+                mma_commit(&bar[C::dp_full]);
+            };
+            w.wait(&bar[C::kv_full], 0);
+            scores(0);
+            dprobs(0);
+            for (int i = 0; i < steps && !w.aborted(); ++i) {
+                const unsigned char *q = sm + C::Q + (i % NS) * C::TILE, *o = sm + C::O + (i % NS) * C::TILE;
+                w.wait(&bar[C::p_half], i);
+                if (w.aborted()) break;
+                tc_fence_after();
+                mma_chunks<D>(tmem + C::tV, tmem + C::tS, o, 0, 4, i > 0);
+                w.wait(&bar[C::p_half + 1], i);
+                if (w.aborted()) break;
+                tc_fence_after();
+                mma_chunks<D>(tmem + C::tV, tmem + C::tS, o, 4, 8, true);
+                mma_commit(&bar[C::dv_done]);
+                w.wait(&bar[C::ds_full], i);
+                if (w.aborted()) break;
+                tc_fence_after();
+                mma_chunks<D>(tmem + C::tK, tmem + C::tP, q, 0, 8, i > 0);
+                mma_commit(&bar[C::dk_done]);
+                mma_commit(&bar[C::empty + i % NS]);
+                if (i + 1 < steps) {
+                    w.wait(&bar[C::dv_done], i);
+                    scores(i + 1);
+                    w.wait(&bar[C::dk_done], i);
+                    dprobs(i + 1);
+                }
+            }
+            if (w.aborted()) {
+                mma_commit(&bar[C::drain]);
+                mbar_wait_bounded(&bar[C::drain], 0, 100000000ull);
+            }
+        }
+    } else {
+        const int g = warp >> 2, wq = warp & 3, r = tid & (BT - 1);  // r: key row
+        const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+        const uint32_t tS = tmem + lanes + C::tS, tP = tmem + lanes + C::tP;
+        const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e);
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % NS;
+            const float *st = reinterpret_cast<const float *>(sm + C::ST) + s * 2 * BT;
+            float p[2][32];
+            w.wait(&bar[C::q_full + s], i / NS);
+            w.wait(&bar[C::s_full], i);
+            if (w.stopped()) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) tmem_ld32(tS + 64 * q + 32 * g, p[q]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c0 = 64 * q + 32 * g;
+#pragma unroll
+                for (int x = 0; x < 32; x += 4) {
+                    const float4 nl = *reinterpret_cast<const float4 *>(st + c0 + x);
+                    unpack2(fma2(pack2(p[q][x], p[q][x + 1]), sc2, pack2(nl.x, nl.y)), p[q][x], p[q][x + 1]);
+                    unpack2(fma2(pack2(p[q][x + 2], p[q][x + 3]), sc2, pack2(nl.z, nl.w)), p[q][x + 2], p[q][x + 3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[q][x + e] = ex2_approx(p[q][x + e]);
+                }
+                if (i % n == 0) {  // the diagonal block: queries before the key
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (c0 + x < r) p[q][x] = 0.f;
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) pk[x >> 1] = pack_bf16x2(p[q][x], p[q][x + 1]);
+                tmem_st16(tS + c0, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(&bar[C::p_half + q]);
+            }
+            w.wait(&bar[C::dp_full], i);
+            if (w.stopped()) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c0 = 64 * q + 32 * g;
+                float dp[32];
+                tmem_ld32(tP + c0, dp);
+                tmem_wait_ld();
+                uint32_t ds[16];
+#pragma unroll
+                for (int x = 0; x < 32; x += 4) {
+                    const float4 nd = *reinterpret_cast<const float4 *>(st + BT + c0 + x);
+                    float a, b;
+                    unpack2(mul2(pack2(p[q][x], p[q][x + 1]), add2(pack2(dp[x], dp[x + 1]), pack2(nd.x, nd.y))), a, b);
+                    ds[x >> 1] = pack_bf16x2(a, b);
+                    unpack2(mul2(pack2(p[q][x + 2], p[q][x + 3]), add2(pack2(dp[x + 2], dp[x + 3]), pack2(nd.z, nd.w))), a, b);
+                    ds[(x >> 1) + 1] = pack_bf16x2(a, b);
+                }
+                tmem_st16(tP + c0, ds);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(&bar[C::ds_full]);
+        }
+        if (!w.stopped()) {
+            w.wait(&bar[C::dk_done], steps - 1);
+            tc_fence_after();
+            if (!w.stopped()) {  // group 0 stores dV, group 1 dK
+                __nv_bfloat16 *to = (g ? dk : dv) + (row0 * Hk + hk) * D;
+                store_rows<D>(tmem + lanes + (g ? C::tK : C::tV), g ? scale : 1.f, sm + (g ? C::K : C::V), wq, lane, to,
+                              (int64_t)Hk * D, rows);
+            }
+        }
+    }
+    if (w.aborted() && warp == 9) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (lane == 0) drain_loads(bar, C::kv_full, 1 + 2 * NS);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t st)
+{
+    using A = DqCfg<D>;
+    using Bc = DkvCfg<D>;
+    const int64_t tokens = a.cu ? (int64_t)a.T : (int64_t)a.B * a.T;
+    CUtensorMap mq, mk, mv, mo;
+    if (!make_map(&mq, a.q, tokens, a.Hq, D) || !make_map(&mk, a.k, tokens, a.Hk, D) ||
+        !make_map(&mv, a.v, tokens, a.Hk, D) || !make_map(&mo, a.dout, tokens, a.Hq, D))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(attn_bwd_dq_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::TOTAL);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attn_bwd_dkv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Bc::TOTAL);
+    if (e != cudaSuccess) return e;
+    float *nlse = static_cast<float *>(a.workspace), *ndot = nlse + tokens * a.Hq;
+    const long tiles = attn_tiles(a.cu, a.B, a.T, BT);
+    attn_bwd_dq_tc<D><<<(unsigned)(tiles * a.Hq), NTH, A::TOTAL, st>>>(
+        mq, mk, mv, mo, static_cast<const __nv_bfloat16 *>(a.out), a.lse, static_cast<__nv_bfloat16 *>(a.dq), nlse, ndot,
+        a.cu, a.B, a.T, a.Hq, a.Hk, a.scale, tokens);
+    attn_bwd_dkv_tc<D><<<(unsigned)(tiles * a.Hk), NTH, Bc::TOTAL, st>>>(
+        mq, mk, mv, mo, nlse, ndot, static_cast<__nv_bfloat16 *>(a.dk), static_cast<__nv_bfloat16 *>(a.dv), a.cu, a.B, a.T,
+        a.Hq, a.Hk, a.scale, tokens);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd_tc(const AttnArgs &a, cudaStream_t st)
+{
+    return a.d == 128 ? run_bwd<128>(a, st) : run_bwd<64>(a, st);
+}
+
+int read_and_clear_attn_bwd_error()
+{
+    int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attn_bwd_error, sizeof(int)) != cudaSuccess) return -1;
+    if (v) cudaMemcpyToSymbol(g_attn_bwd_error, &z, sizeof(int));
+    return v;
+}
+
+}  // namespace gdn

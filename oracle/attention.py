@@ -42,7 +42,11 @@ def prompt(q, k, v, cu=None, scale=None, dout=None):
     r = {x: np.zeros((n, Hq, d)) for x in ("out", "pv")}
     r["lse"] = np.zeros((n, Hq))
     s_abs = 0.0
+    top = lambda x: float(np.abs(np.nan_to_num(x)).max(initial=0.0))
+    longest = max([b - a for a, b in sequences(lead, cu)])
+    r["amp"] = G * longest * top(v2)
     if dout is not None:
+        r["amp"] += G * longest * (1 + 2 * scale * max(top(q2), top(k2)) * d * top(v2)) * top(f64(dout))
         do2 = f64(dout).reshape(n, Hq, d)
         r |= {x: np.zeros((n, Hq, d)) for x in ("dq", "ds_k", "dov_k", "dpv_k")}
         r |= {x: np.zeros((n, Hk, d)) for x in ("dk", "dv", "p_do", "ds_q", "dov_q", "dpv_q")}
@@ -75,7 +79,7 @@ def prompt(q, k, v, cu=None, scale=None, dout=None):
             for x, y in sums.items():
                 r[x + "_k"][a:b, h] = scale * y @ np.abs(k2[a:b, g])
                 r[x + "_q"][a:b, g] += scale * y.T @ np.abs(q2[a:b, h])
-    for x in list(r):
+    for x in [x for x in r if x != "amp"]:
         r[x] = r[x].reshape(*lead, *r[x].shape[1:])
     r["s_abs"] = s_abs
     return r

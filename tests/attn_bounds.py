@@ -5,6 +5,9 @@ they enter, half a bf16 step in bf16 calls, none in fp32 calls.  A score is a su
 in fp32: off by at most d 2^-24 sum |q| |k| scale, and a few roundings of its size more for the scaling
 and the shift by the maximum; exp2 is off by 2^-22; a sum of n positive terms in fp32 by n 2^-24.
 Second-order terms: 2 %.
+
+exp2 gives 0 below 2^-126 (the smallest normal number): a weight may be off by that much whatever its
+size, which a result sees times what stands beside the weight, summed over the weights (amp).
 """
 import numpy as np
 
@@ -21,7 +24,7 @@ def forward(r, dtype, d, n):
     u, w = U[dtype], U["bf16"] if dtype == "bf16" else 0.0
     e = weight_error(r["s_abs"], d, n)
     out = u * np.abs(r["out"]) + (w + e + n * 2.0 ** -24) * r["pv"]
-    return 1.02 * out + 1e-37, e + 2.0 ** -22 * (1 + np.abs(r["lse"]))
+    return 1.02 * out + 2.0 ** -126 * r["amp"], e + 2.0 ** -22 * (1 + np.abs(r["lse"]))
 
 
 def backward(r, dtype, d, n, G):
@@ -38,7 +41,7 @@ def backward(r, dtype, d, n, G):
         res.append(u * np.abs(r[name]) + (w + acc) * r["ds" + side] + (ep + 2 * d * 2.0 ** -24) * r["dov" + side]
                    + (ep + dd) * r["dpv" + side])
     dv = u * np.abs(r["dv"]) + (w + ep + G * n * 2.0 ** -24) * r["p_do"]
-    return [1.02 * x + 1e-37 for x in (*res, dv)]
+    return [1.02 * x + 2.0 ** -126 * r["amp"] for x in (*res, dv)]
 
 
 def decode(out, pv, s_abs, dtype, d, n):
