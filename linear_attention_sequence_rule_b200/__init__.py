@@ -20,6 +20,7 @@ If ``libgdn.so`` has not been built, importing this package raises: there is no 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -862,72 +863,89 @@ class CachePlan(NamedTuple):
     status: torch.Tensor
 
 
-class _On:
-    """The call's device and stream: the tensors' device is made the current one for the launch, and
-    without a stream the call goes to that device's current stream.  Scratch that a call takes from
-    the allocator is kept from reuse until the stream given has passed it."""
+# These calls are made once per layer and step, small ones among them, so their host side is kept short:
+# one comparison per tensor where all is well (the named checks of _need tell what is not), the
+# current stream and device from torch's own accessors, sizes queried once per shape.
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"tensors are on {device}, expected a CUDA device")
-        self.device, self.given = device, stream
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        if self.stream.device != device:
-            raise ValueError(f"stream is on {self.stream.device}, the tensors on {device}")
-
-    def call(self, fn, *args):
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(*args, self.stream.cuda_stream)
-        else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, self.stream.cuda_stream)
-        if rc != GDN_OK:
-            raise GdnError(rc, gdn_last_error())
-
-    def query(self, fn, *args):
-        with torch.cuda.device(self.device):
-            n = fn(*args)
-        if n == ctypes.c_size_t(-1).value:
-            raise GdnError(GDN_ERR_INVALID_ARGUMENT, gdn_last_error())
-        return n
-
-    def new(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.given is not None:
-            t.record_stream(self.given)
-        return t
-
-    def scratch(self, workspace, need):
-        """(pointer, bytes) of the caller's workspace or of one taken for this call (the third item
-        keeps it alive until the launch)."""
-        if workspace is None and need:
-            workspace = self.new((need,), torch.uint8)
-        if workspace is None:
-            return None, 0, None
-        _need(workspace, "workspace", device=self.device)
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _heads(q, k, cu_seqlens, d_names=("q", "k")):
+def _is(t, name, dtype, shape, dev):
+    if t is None or t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _need(t, name, dtype, shape, dev)
+
+
+def _cuda_device(t):
+    if not t.is_cuda:
+        raise ValueError(f"tensors are on {t.device}, expected a CUDA device")
+    return t.device
+
+
+def _run(fn, dev, stream, *args):
+    """Launch on the tensors' device: on `stream`, or on that device's current stream."""
+    i = dev.index
+    if stream is None:
+        raw = _raw_stream(i)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    else:
+        raw = stream.cuda_stream
+    if _current_device() == i:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, raw)
+    if rc != GDN_OK:
+        raise GdnError(rc, gdn_last_error())
+
+
+def _new(stream, like, shape=None, dtype=None):
+    """A tensor taken for this call; the allocator keeps it until a stream that was given has passed."""
+    if shape is None:
+        t = torch.empty_like(like)
+    else:
+        t = like.new_empty(shape, dtype=dtype or like.dtype)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+@functools.lru_cache(maxsize=1024)
+def _size(fn, device_index, *args):
+    with torch.cuda.device(device_index):
+        n = fn(*args)
+    if n == ctypes.c_size_t(-1).value:
+        raise GdnError(GDN_ERR_INVALID_ARGUMENT, gdn_last_error())
+    return n
+
+
+def _scratch(workspace, need, stream, like):
+    """(tensor or None, pointer or None, bytes) of the caller's workspace, or of one taken for this call."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = _new(stream, like, (need,), torch.uint8)
+    else:
+        _need(workspace, "workspace", device=like.device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _prompt(q, k, cu_seqlens):
     """(lead dims, B, T, Hq, Hk, d, dtype code) of a prompt call."""
     want = 4 if cu_seqlens is None else 3
     if q is None or q.dim() != want or k is None or k.dim() != want:
-        raise ValueError(f"{d_names[0]} and {d_names[1]} must have {want} dimensions")
+        raise ValueError(f"q and k must have {want} dimensions")
     if q.dtype not in _DT:
         raise ValueError(f"unsupported dtype {q.dtype}")
-    lead = tuple(q.shape[:-2])
     if cu_seqlens is None:
-        B, T = lead
-    else:
-        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
-            raise ValueError("cu_seqlens must hold B + 1 >= 2 offsets")
-        B, T = cu_seqlens.shape[0] - 1, lead[0]
-        _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), q.device)
-    return lead, B, T, q.shape[-2], k.shape[-2], q.shape[-1]
-
-
-def _scale(scale, d):
-    return d ** -0.5 if scale is None else float(scale)
+        B, T, Hq, d = q.shape
+        return (B, T), B, T, Hq, k.shape[2], d, _DT[q.dtype]
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must hold B + 1 >= 2 offsets")
+    _is(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, q.device)
+    T, Hq, d = q.shape
+    return (T,), cu_seqlens.shape[0] - 1, T, Hq, k.shape[1], d, _DT[q.dtype]
 
 
 def attn_fwd(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None, stream=None):
@@ -935,19 +953,24 @@ def attn_fwd(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None, stream=No
     q [T,Hq,d] ... with cu_seqlens (int32 [B+1] on the device); Hq a multiple of Hk; scale defaults to
     1 / sqrt(d).  Returns (out, lse), lse [.., Hq] the log of each row's softmax sum.  Rows behind the
     last sequence of a pack are not written."""
-    lead, B, T, Hq, Hk, d = _heads(q, k, cu_seqlens)
-    dt, on = q.dtype, _On(q.device, stream)
-    _need(q, "q", dt, (*lead, Hq, d))
-    _need(k, "k", dt, (*lead, Hk, d), q.device)
-    _need(v, "v", dt, (*lead, Hk, d), q.device)
-    out = on.new((*lead, Hq, d), dt) if out is None else out
-    lse = on.new((*lead, Hq), torch.float32) if lse is None else lse
-    _need(out, "out", dt, (*lead, Hq, d), q.device)
-    _need(lse, "lse", torch.float32, (*lead, Hq), q.device)
-    if lead.count(0) and cu_seqlens is not None:
+    lead, B, T, Hq, Hk, d, code = _prompt(q, k, cu_seqlens)
+    dt, dev = q.dtype, _cuda_device(q)
+    kv = (*lead, Hk, d)
+    _is(q, "q", dt, q.shape, dev)
+    _is(k, "k", dt, kv, dev)
+    _is(v, "v", dt, kv, dev)
+    if out is None:
+        out = _new(stream, q)
+    else:
+        _is(out, "out", dt, q.shape, dev)
+    if lse is None:
+        lse = _new(stream, q, (*lead, Hq), torch.float32)
+    else:
+        _is(lse, "lse", torch.float32, (*lead, Hq), dev)
+    if T == 0 and cu_seqlens is not None:
         return out, lse
-    on.call(gdn_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, T, Hq, Hk, d,
-            _ptr(cu_seqlens), _DT[dt], _scale(scale, d))
+    _run(_lib.gdn_attn_fwd, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+         B, T, Hq, Hk, d, _ptr(cu_seqlens), code, d ** -0.5 if scale is None else scale)
     return out, lse
 
 
@@ -955,27 +978,34 @@ def attn_bwd(q, k, v, out, lse, dout, cu_seqlens=None, scale=None, dq=None, dk=N
              stream=None):
     """Gradients (dq, dk, dv), in q's dtype, of ``attn_fwd``'s out with respect to q, k and v, from its
     inputs, its results out and lse, and dout = dL/dout."""
-    lead, B, T, Hq, Hk, d = _heads(q, k, cu_seqlens)
-    dt, dev, on = q.dtype, q.device, _On(q.device, stream)
-    _need(q, "q", dt, (*lead, Hq, d))
-    _need(k, "k", dt, (*lead, Hk, d), dev)
-    _need(v, "v", dt, (*lead, Hk, d), dev)
-    _need(out, "out", dt, (*lead, Hq, d), dev)
-    _need(dout, "dout", dt, (*lead, Hq, d), dev)
-    _need(lse, "lse", torch.float32, (*lead, Hq), dev)
-    dq = on.new((*lead, Hq, d), dt) if dq is None else dq
-    dk = on.new((*lead, Hk, d), dt) if dk is None else dk
-    dv = on.new((*lead, Hk, d), dt) if dv is None else dv
-    _need(dq, "dq", dt, (*lead, Hq, d), dev)
-    _need(dk, "dk", dt, (*lead, Hk, d), dev)
-    _need(dv, "dv", dt, (*lead, Hk, d), dev)
-    if lead.count(0) and cu_seqlens is not None:
+    lead, B, T, Hq, Hk, d, code = _prompt(q, k, cu_seqlens)
+    dt, dev = q.dtype, _cuda_device(q)
+    shape, kv = q.shape, (*lead, Hk, d)
+    _is(q, "q", dt, shape, dev)
+    _is(k, "k", dt, kv, dev)
+    _is(v, "v", dt, kv, dev)
+    _is(out, "out", dt, shape, dev)
+    _is(dout, "dout", dt, shape, dev)
+    _is(lse, "lse", torch.float32, (*lead, Hq), dev)
+    if dq is None:
+        dq = _new(stream, q)
+    else:
+        _is(dq, "dq", dt, shape, dev)
+    if dk is None:
+        dk = _new(stream, k)
+    else:
+        _is(dk, "dk", dt, kv, dev)
+    if dv is None:
+        dv = _new(stream, v)
+    else:
+        _is(dv, "dv", dt, kv, dev)
+    if T == 0 and cu_seqlens is not None:
         return dq, dk, dv
-    need = on.query(gdn_attn_bwd_workspace_bytes, B, T, Hq, Hk, d, int(cu_seqlens is not None), _DT[dt])
-    ws, wbytes, _keep = on.scratch(workspace, need)
-    on.call(gdn_attn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
-            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, T, Hq, Hk, d, _ptr(cu_seqlens), _DT[dt],
-            _scale(scale, d), ws, wbytes)
+    need = _size(gdn_attn_bwd_workspace_bytes, dev.index, B, T, Hq, Hk, d, int(cu_seqlens is not None), code)
+    keep, ws, wbytes = _scratch(workspace, need, stream, q)
+    _run(_lib.gdn_attn_bwd, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+         dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, T, Hq, Hk, d, _ptr(cu_seqlens), code,
+         d ** -0.5 if scale is None else scale, ws, wbytes)
     return dq, dk, dv
 
 
@@ -984,49 +1014,55 @@ def cache_plan(lens, added, block_table, free_list, free_head, page, rows, cu_se
     """Plan one step of a paged cache on the device: N requests holding ``lens`` tokens get ``added``
     new ones; pages come from ``free_list`` (entries from free_head on) and go into ``block_table``
     [N, max_blocks], in place.  ``rows``: how many packed rows the step has room for.  All int32.
-    Returns a CachePlan; a plan that does not fit is refused as a whole (its status is not 0)."""
-    i32, dev, on = torch.int32, lens.device, _On(lens.device, stream)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have 2 dimensions")
+    Returns a CachePlan; a plan that does not fit is refused as a whole (its status is not 0).
+    Results that are not given share one new allocation."""
+    i32, dev = torch.int32, _cuda_device(lens)
+    if block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("block_table must have 2 dimensions and free_list 1")
     N, max_blocks = block_table.shape
-    _need(lens, "lens", i32, (N,))
-    _need(added, "added", i32, (N,), dev)
-    _need(block_table, "block_table", i32, (N, max_blocks), dev)
-    _need(free_list, "free_list", i32, (free_list.numel(),), dev)
-    _need(free_head, "free_head", i32, (1,), dev)
+    num_free = free_list.shape[0]
     rows = int(rows)
     if rows < 0:
         raise ValueError("rows must be >= 0")
-    given = dict(cu_seqlens=(cu_seqlens, (N + 1,)), slots=(slots, (rows,)), positions=(positions, (rows,)),
-                 lens_out=(lens_out, (N,)), free_head_out=(free_head_out, (1,)), status=(status, (2,)))
-    o = {}
-    for name, (t, shape) in given.items():
-        if t is None:
-            o[name] = on.new(shape, i32)
-        else:
-            _need(t, name, i32, shape, dev)
-            o[name] = t
-    on.call(gdn_cache_plan, lens.data_ptr(), added.data_ptr(), block_table.data_ptr(), _some(free_list),
-            free_head.data_ptr(), o["cu_seqlens"].data_ptr(), _some(o["slots"]), _some(o["positions"]),
-            o["lens_out"].data_ptr(), o["free_head_out"].data_ptr(), o["status"].data_ptr(), N, max_blocks,
-            free_list.numel(), rows, int(page))
-    return CachePlan(o["cu_seqlens"], o["slots"], o["positions"], o["lens_out"], o["free_head_out"], o["status"])
+    _is(lens, "lens", i32, (N,), dev)
+    _is(added, "added", i32, (N,), dev)
+    _is(block_table, "block_table", i32, block_table.shape, dev)
+    _is(free_list, "free_list", i32, free_list.shape, dev)
+    _is(free_head, "free_head", i32, (1,), dev)
+    o = [cu_seqlens, slots, positions, lens_out, free_head_out, status]
+    if all(t is None for t in o):  # 16-byte aligned parts of one allocation
+        a, b, c = -(N + 1) & 3, -rows & 3, -N & 3
+        o = _new(stream, lens, (N + 1 + a + 2 * (rows + b) + N + c + 8,)).split_with_sizes(
+            (N + 1, a, rows, b, rows, b, N, c, 1, 3, 2, 2))[::2]
+    else:
+        names = ("cu_seqlens", "slots", "positions", "lens_out", "free_head_out", "status")
+        for i, (t, n, name) in enumerate(zip(o, (N + 1, rows, rows, N, 1, 2), names)):
+            if t is None:
+                o[i] = _new(stream, lens, (n,))
+            else:
+                _is(t, name, i32, (n,), dev)
+    plan = CachePlan(*o)
+    _run(_lib.gdn_cache_plan, dev, stream, lens.data_ptr(), added.data_ptr(), block_table.data_ptr(),
+         free_list.data_ptr() if num_free else None, free_head.data_ptr(), o[0].data_ptr(),
+         o[1].data_ptr() if rows else None, o[2].data_ptr() if rows else None, o[3].data_ptr(), o[4].data_ptr(),
+         o[5].data_ptr(), N, max_blocks, num_free, rows, page)
+    return plan
 
 
-def _some(t):
-    return t.data_ptr() if t.numel() else None
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, d, dev):
-    if k_cache.dim() != 4 or k_cache.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if k_cache.dim() != 4 or k_cache.dtype not in _E4M3:
         raise ValueError("k_cache must be float8_e4m3fn (or its bytes, uint8) [num_pages, Hk, page, d]")
-    P, Hk, page, dc = k_cache.shape
+    shape = k_cache.shape
+    P, Hk, page, dc = shape
     if dc != d:
         raise ValueError(f"k_cache has head size {dc}, expected {d}")
-    _need(k_cache, "k_cache", None, None, dev)
-    _need(v_cache, "v_cache", k_cache.dtype, (P, Hk, page, d), dev)
-    _need(k_scale, "k_scale", torch.float32, (P, Hk), dev)
-    _need(v_scale, "v_scale", torch.float32, (P, Hk), dev)
+    _is(k_cache, "k_cache", k_cache.dtype, shape, dev)
+    _is(v_cache, "v_cache", k_cache.dtype, shape, dev)
+    _is(k_scale, "k_scale", torch.float32, (P, Hk), dev)
+    _is(v_scale, "v_scale", torch.float32, (P, Hk), dev)
     return P, Hk, page
 
 
@@ -1037,15 +1073,17 @@ def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     if k.dim() != 3:
         raise ValueError("k must have 3 dimensions")
     rows, Hk, d = k.shape
-    dt, dev, on = k.dtype, k.device, _On(k.device, stream)
+    dt, dev = k.dtype, _cuda_device(k)
     if dt not in _DT:
         raise ValueError(f"unsupported dtype {dt}")
     P, Hc, page = _cache(k_cache, v_cache, k_scale, v_scale, d, dev)
-    _need(k, "k", dt, (rows, Hc, d))
-    _need(v, "v", dt, (rows, Hc, d), dev)
-    _need(slots, "slots", torch.int32, (rows,), dev)
-    on.call(gdn_cache_append, _some(k), _some(v), _some(slots), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), rows, Hk, d, page, P, _DT[dt])
+    _is(k, "k", dt, (rows, Hc, d), dev)
+    _is(v, "v", dt, (rows, Hc, d), dev)
+    _is(slots, "slots", torch.int32, (rows,), dev)
+    if rows == 0:
+        return
+    _run(_lib.gdn_cache_append, dev, stream, k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
+         v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), rows, Hk, d, page, P, _DT[dt])
 
 
 def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=None, out=None, workspace=None,
@@ -1053,24 +1091,25 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=
     """One-token softmax attention q [N, Hq, d] over the paged e4m3 cache: request n attends to its first
     lens[n] cached tokens through block_table [N, max_blocks]; scale defaults to 1 / sqrt(d).  Returns
     out [N, Hq, d]; a request without tokens gets zeros."""
-    if q.dim() != 3:
-        raise ValueError("q must have 3 dimensions")
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must have 3 dimensions and block_table 2")
     N, Hq, d = q.shape
-    dt, dev, on = q.dtype, q.device, _On(q.device, stream)
+    dt, dev = q.dtype, _cuda_device(q)
     if dt not in _DT:
         raise ValueError(f"unsupported dtype {dt}")
     P, Hk, page = _cache(k_cache, v_cache, k_scale, v_scale, d, dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have 2 dimensions")
     max_blocks = block_table.shape[1]
-    _need(q, "q", dt, (N, Hq, d))
-    _need(block_table, "block_table", torch.int32, (N, max_blocks), dev)
-    _need(lens, "lens", torch.int32, (N,), dev)
-    out = on.new((N, Hq, d), dt) if out is None else out
-    _need(out, "out", dt, (N, Hq, d), dev)
-    need = on.query(gdn_attn_decode_workspace_bytes, N, Hq, Hk, d, page, max_blocks, _DT[dt])
-    ws, wbytes, _keep = on.scratch(workspace, need)
-    on.call(gdn_attn_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(), out.data_ptr(), N, Hq, Hk, d, page, P,
-            max_blocks, _DT[dt], _scale(scale, d), ws, wbytes)
+    _is(q, "q", dt, q.shape, dev)
+    _is(block_table, "block_table", torch.int32, (N, max_blocks), dev)
+    _is(lens, "lens", torch.int32, (N,), dev)
+    if out is None:
+        out = _new(stream, q)
+    else:
+        _is(out, "out", dt, q.shape, dev)
+    code = _DT[dt]
+    need = _size(gdn_attn_decode_workspace_bytes, dev.index, N, Hq, Hk, d, page, max_blocks, code)
+    keep, ws, wbytes = _scratch(workspace, need, stream, q)
+    _run(_lib.gdn_attn_decode, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+         v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(), out.data_ptr(), N, Hq, Hk, d, page, P,
+         max_blocks, code, d ** -0.5 if scale is None else scale, ws, wbytes)
     return out
