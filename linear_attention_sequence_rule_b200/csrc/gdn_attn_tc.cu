@@ -8,7 +8,7 @@
 // L2 traffic of one tile).  Per tile, S (128 columns), O (D columns) and P (bf16, 64 columns; at
 // D = 128 over S's first columns, since S0, S1, O0, O1 fill the 512) sit in tensor memory.
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread holds a row
-//   warps 8, 9       one thread each issues the MMAs of tile 0, 1
+//   warps 8, 9       issue the MMAs of tile 0, 1
 //   warp 10          loads; zeroes V rows behind the sequence's end
 // The tiles run apart: while one's softmax runs on the CUDA cores, the other's products fill the tensor
 // pipe.  The maximum is moved only when a row's new one passes it by 2^8 (weights up to 2^8 are as
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(NTH, 1)
         for (int i = 0; i < C::NBAR; ++i) {
             int n = 1;
             if ((i >= C::k_empty && i < C::v_full) || (i >= C::v_empty && i < C::v_zeroed)) n = n1 ? 2 : 1;
-            if (i >= C::s_free && i < C::pv_done) n = BT;
+            if (i >= C::s_free && i < C::pv_done) n = BT / 32;  // one a warp
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(NTH, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     // registers: 384 x 168 = 64512 at launch; 128 x 48 + 256 x 224 = 63488 after the two roles' changes
     if (warp >= 8) {
@@ -128,21 +128,21 @@ __global__ void __launch_bounds__(NTH, 1)
     } else if (warp < 10) {
         // ---- products of tile t ----
         const int t = warp - 8, n = t ? n1 : n0;
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             const unsigned char *qt = sm + C::Q + t * C::TILE;
             const uint32_t tS = tmem + C::tS(t), tO = tmem + C::tO(t), tP = tmem + C::tP(t);
             auto scores = [&](int j) {
                 const int s = j % NS;
                 w.wait(&bar[C::k_full + s], j / NS);
-                if (w.aborted()) return;
+                if (w.stopped()) return;
                 tc_fence_after();
                 mma_nt<D>(tS, qt, sm + C::K + s * C::TILE);
-                mma_commit(&bar[C::s_full + t]);
-                mma_commit(&bar[C::k_empty + s]);
+                commit(&bar[C::s_full + t]);
+                commit(&bar[C::k_empty + s]);
             };
             w.wait(&bar[C::q_full + t], 0);
             scores(0);
-            for (int j = 0; j < n && !w.aborted(); ++j) {
+            for (int j = 0; j < n && !w.stopped(); ++j) {
                 const int s = j % NS;
                 if (C::SEP && j + 1 < n) {
                     w.wait(&bar[C::s_free + t], j);
@@ -151,15 +151,15 @@ __global__ void __launch_bounds__(NTH, 1)
                 w.wait(&bar[C::v_full + s], j / NS);
                 if (j == nmax - 1 && at.len < nmax * BT) w.wait(&bar[C::v_zeroed], 0);
                 w.wait(&bar[C::p_half + 2 * t], j);
-                if (w.aborted()) break;
+                if (w.stopped()) break;
                 tc_fence_after();
                 mma_tn<D>(tO, tP, sm + C::V + s * C::TILE, 0, 4, j > 0);
                 w.wait(&bar[C::p_half + 2 * t + 1], j);
-                if (w.aborted()) break;
+                if (w.stopped()) break;
                 tc_fence_after();
                 mma_tn<D>(tO, tP, sm + C::V + s * C::TILE, 4, 8, true);
-                mma_commit(&bar[C::pv_done + t]);
-                mma_commit(&bar[C::v_empty + s]);
+                commit(&bar[C::pv_done + t]);
+                commit(&bar[C::v_empty + s]);
                 if (!C::SEP && j + 1 < n) {  // the next S overwrites P
                     w.wait(&bar[C::pv_done + t], j);
                     scores(j + 1);
@@ -168,12 +168,12 @@ __global__ void __launch_bounds__(NTH, 1)
             if (t == 0 && n1) {  // tile 0 has no part in the last block
                 const int s = (nmax - 1) % NS;
                 w.wait(&bar[C::k_full + s], (nmax - 1) / NS);
-                arrive(&bar[C::k_empty + s]);
+                if (lane == 0) arrive(&bar[C::k_empty + s]);
                 w.wait(&bar[C::v_full + s], (nmax - 1) / NS);
-                arrive(&bar[C::v_empty + s]);
+                if (lane == 0) arrive(&bar[C::v_empty + s]);
             }
-            if (w.aborted()) {  // products issued already end before the tensor memory is freed
-                mma_commit(&bar[C::drain + t]);
+            if (w.stopped()) {  // products issued already end before the tensor memory is freed
+                commit(&bar[C::drain + t]);
                 mbar_wait_bounded(&bar[C::drain + t], 0, 100000000ull);
             }
         }
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(NTH, 1)
             tmem_wait_ld();
             if (C::SEP) {
                 tc_fence_before();
-                arrive(&bar[C::s_free + t]);
+                warp_arrive(&bar[C::s_free + t], lane);
             }
             if (j == n - 1) {  // the diagonal block
 #pragma unroll
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 tmem_st32(tP + 32 * hf, p);
                 tmem_wait_st();
                 tc_fence_before();
-                arrive(&bar[C::p_half + 2 * t + hf]);
+                warp_arrive(&bar[C::p_half + 2 * t + hf], lane);
             }
             float a, b;
             unpack2(add2(sum[0], sum[1]), a, b);

@@ -47,6 +47,14 @@ __device__ __forceinline__ void arrive(uint64_t *b)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
 }
 
+// One arrival for a warp, behind what all its lanes have done (32 arrivals on one barrier would be
+// served one after the other).
+__device__ __forceinline__ void warp_arrive(uint64_t *b, int lane)
+{
+    __syncwarp();
+    if (lane == 0) arrive(b);
+}
+
 // Pairs of fp32 in one 64-bit register: one instruction for two results.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
 {
@@ -103,6 +111,39 @@ template <int D> __device__ __forceinline__ void zero_rows(unsigned char *tile, 
     __syncwarp();
 }
 
+// The products are issued by a whole warp whose leader alone executes them (elect.sync): in code that
+// one lane runs by itself the descriptors cannot live in uniform registers, and moving them there
+// instruction by instruction costs more than twice the time of the products (at d = 128 about
+// 145 cycles an instruction of 64).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
 // D[128 x 128] = A B^T over the head size: both tiles K-major in shared memory
 template <int D> __device__ __forceinline__ void mma_nt(uint32_t d, const unsigned char *a, const unsigned char *b)
 {
@@ -110,7 +151,7 @@ template <int D> __device__ __forceinline__ void mma_nt(uint32_t d, const unsign
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t o = (kk >> 2) * kSub + (kk & 3) * 32;
-        mma_bf16(d, sdesc_sw128(smem_u32(a) + o, 16, 1024), sdesc_sw128(smem_u32(b) + o, 16, 1024), id, kk > 0);
+        mma_ss(d, sdesc_sw128(smem_u32(a) + o, 16, 1024), sdesc_sw128(smem_u32(b) + o, 16, 1024), id, kk > 0);
     }
 }
 
@@ -122,7 +163,7 @@ __device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, const unsigned ch
     constexpr uint32_t id = idesc_bf16(BT, D, 0, 1);
 #pragma unroll
     for (int kk = k0; kk < k1; ++kk)
-        mma_bf16_ta(d, a + 8 * kk, sdesc_sw128(smem_u32(b) + kk * 2048, kSub, 1024), id, accumulate || kk > k0);
+        mma_ts(d, a + 8 * kk, sdesc_sw128(smem_u32(b) + kk * 2048, kSub, 1024), id, accumulate || kk > k0);
 }
 
 // 32 fp32 accumulator rows (thread = row of its warp's 32; columns of `acc` at tensor memory address t)

@@ -17,7 +17,7 @@
 // the key side, head by head ([Hq][tokens] each), into the workspace.
 //
 // In both kernels warps 0-7 work element by element (a thread has a row; two groups of 4 warps take
-// different 32-column chunks), one thread of warp 8 issues the products, warp 9 loads.  P and dS (bf16)
+// different 32-column chunks), warp 8 issues the products, warp 9 loads.  P and dS (bf16)
 // are written over the first half of the very S or dP columns they came from, which their own
 // thread has read.
 #include <math.h>
@@ -45,7 +45,7 @@ __device__ __forceinline__ void mma_chunks(uint32_t d, uint32_t a, const unsigne
     constexpr uint32_t id = idesc_bf16(BT, D, 0, 1);
 #pragma unroll
     for (int kk = k0; kk < k1; ++kk)
-        mma_bf16_ta(d, a + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_sw128(smem_u32(b) + kk * 2048, kSub, 1024), id,
+        mma_ts(d, a + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_sw128(smem_u32(b) + kk * 2048, kSub, 1024), id,
                     accumulate || kk > k0);
 }
 
@@ -71,17 +71,20 @@ __device__ __forceinline__ void drain_loads(uint64_t *bar, int first, int count)
 
 // ---- query side ------------------------------------------------------------------------------------
 
+// A K stage is held from the scores to dQ, a V stage only for dP: with two K stages of d = 128 every
+// load would be waited for.
 template <int D> struct DqCfg {
-    static constexpr int NS = D == 64 ? 4 : 2;
+    static constexpr int NK = D == 64 ? 4 : 3, NV = D == 64 ? 4 : 2;
     static constexpr int TILE = BT * D * 2;
-    static constexpr int Q = 0, O = TILE, K = 2 * TILE, V = K + NS * TILE, RED = V + NS * TILE, BAR = RED + 2 * BT * 4;
+    static constexpr int Q = 0, O = TILE, K = 2 * TILE, V = K + NK * TILE, RED = V + NV * TILE, BAR = RED + 2 * BT * 4;
     static constexpr int q_full = 0;               // Q and dO
-    static constexpr int k_full = 1;               // [NS]
-    static constexpr int v_full = k_full + NS;     // [NS]
-    static constexpr int k_empty = v_full + NS;    // [NS]
-    static constexpr int v_empty = k_empty + NS;   // [NS]
-    static constexpr int zeroed = v_empty + NS;    // [NS] the stage has no row behind the end (ragged ends only)
-    static constexpr int s_full = zeroed + NS;     // [2]
+    static constexpr int k_full = 1;               // [NK]
+    static constexpr int v_full = k_full + NK;     // [NV]
+    static constexpr int k_empty = v_full + NV;    // [NK]
+    static constexpr int v_empty = k_empty + NK;   // [NV]
+    static constexpr int k_zeroed = v_empty + NV;  // [NK] the stage has no row behind the end (ragged ends only)
+    static constexpr int v_zeroed = k_zeroed + NK; // [NV]
+    static constexpr int s_full = v_zeroed + NV;   // [2]
     static constexpr int dp_full = s_full + 2;
     static constexpr int dp_free = dp_full + 1;    // dP has been read
     static constexpr int ds_full = dp_free + 1;    // [2] dS is there (first pass: S has been read)
@@ -91,6 +94,7 @@ template <int D> struct DqCfg {
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
     static constexpr uint32_t tS = 0, tP = 256, tQ = 384;  // S[2], dP, dQ
+    static_assert(TOTAL <= 232448, "shared memory budget");
 };
 
 template <int D>
@@ -102,7 +106,7 @@ __global__ void __launch_bounds__(NTH, 1)
                    int Hq, int Hk, float scale, int64_t tokens)
 {
     using C = DqCfg<D>;
-    constexpr int NS = C::NS;
+    constexpr int NK = C::NK, NV = C::NV;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::BAR);
@@ -123,7 +127,7 @@ __global__ void __launch_bounds__(NTH, 1)
 
     if (tid == 0) {
         for (int i = 0; i < C::NBAR; ++i)
-            mbar_init(&bar[i], i == C::dp_free || (i >= C::ds_full && i < C::dq_done) ? NEL : 1);
+            mbar_init(&bar[i], i == C::dp_free || (i >= C::ds_full && i < C::dq_done) ? NEL / 32 : 1);  // one a warp
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(NTH, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp == 9) {
         if (lane == 0) {
@@ -143,55 +147,58 @@ __global__ void __launch_bounds__(NTH, 1)
             load_tile<D>(sm + C::O, &tmO, &bar[C::q_full], h, (int)row0);
         }
         for (int i = 0; i < steps; ++i) {
-            const int s = i % NS, j = i % n;
+            const int sk = i % NK, sv = i % NV, j = i % n;
             if (lane == 0) {
-                if (i >= NS) w.wait(&bar[C::k_empty + s], i / NS - 1);
+                if (i >= NK) w.wait(&bar[C::k_empty + sk], i / NK - 1);
                 if (!w.aborted()) {
-                    mbar_arrive_expect_tx(&bar[C::k_full + s], C::TILE);
-                    load_tile<D>(sm + C::K + s * C::TILE, &tmK, &bar[C::k_full + s], hk, (int)at.t0 + j * BT);
+                    mbar_arrive_expect_tx(&bar[C::k_full + sk], C::TILE);
+                    load_tile<D>(sm + C::K + sk * C::TILE, &tmK, &bar[C::k_full + sk], hk, (int)at.t0 + j * BT);
                 }
-                if (i >= NS) w.wait(&bar[C::v_empty + s], i / NS - 1);
+                if (i >= NV) w.wait(&bar[C::v_empty + sv], i / NV - 1);
                 if (!w.aborted()) {
-                    mbar_arrive_expect_tx(&bar[C::v_full + s], C::TILE);
-                    load_tile<D>(sm + C::V + s * C::TILE, &tmV, &bar[C::v_full + s], hk, (int)at.t0 + j * BT);
+                    mbar_arrive_expect_tx(&bar[C::v_full + sv], C::TILE);
+                    load_tile<D>(sm + C::V + sv * C::TILE, &tmV, &bar[C::v_full + sv], hk, (int)at.t0 + j * BT);
                 }
             }
             __syncwarp();
             if (w.stopped()) break;
-            if (j == n - 1 && rows < BT) {
-                w.wait(&bar[C::k_full + s], i / NS);
-                w.wait(&bar[C::v_full + s], i / NS);
-                if (w.stopped()) break;
-                zero_rows<D>(sm + C::K + s * C::TILE, rows, lane);
-                zero_rows<D>(sm + C::V + s * C::TILE, rows, lane);
+            if (rows < BT) {
+                if (j == n - 1) {
+                    w.wait(&bar[C::k_full + sk], i / NK);
+                    w.wait(&bar[C::v_full + sv], i / NV);
+                    if (w.stopped()) break;
+                    zero_rows<D>(sm + C::K + sk * C::TILE, rows, lane);
+                    zero_rows<D>(sm + C::V + sv * C::TILE, rows, lane);
+                }
+                if (lane == 0) {
+                    arrive(&bar[C::k_zeroed + sk]);
+                    arrive(&bar[C::v_zeroed + sv]);
+                }
             }
-            if (rows < BT && lane == 0) arrive(&bar[C::zeroed + s]);
         }
     } else if (warp == 8) {
-        if (lane == 0) {
-            auto arrived = [&](int first, int i) {  // step i's tile, and its zeros
-                w.wait(&bar[first + i % NS], i / NS);
-                if (rows < BT) w.wait(&bar[C::zeroed + i % NS], i / NS);
-            };
+        {
             auto scores = [&](int i) {
-                arrived(C::k_full, i);
-                if (w.aborted()) return;
+                w.wait(&bar[C::k_full + i % NK], i / NK);
+                if (rows < BT) w.wait(&bar[C::k_zeroed + i % NK], i / NK);
+                if (w.stopped()) return;
                 tc_fence_after();
-                mma_nt<D>(tmem + C::tS + 128 * (i & 1), sm + C::Q, sm + C::K + (i % NS) * C::TILE);
-                mma_commit(&bar[C::s_full + (i & 1)]);
+                mma_nt<D>(tmem + C::tS + 128 * (i & 1), sm + C::Q, sm + C::K + (i % NK) * C::TILE);
+                commit(&bar[C::s_full + (i & 1)]);
             };
             auto dprobs = [&](int i) {
-                arrived(C::v_full, i);
-                if (w.aborted()) return;
+                w.wait(&bar[C::v_full + i % NV], i / NV);
+                if (rows < BT) w.wait(&bar[C::v_zeroed + i % NV], i / NV);
+                if (w.stopped()) return;
                 tc_fence_after();
-                mma_nt<D>(tmem + C::tP, sm + C::O, sm + C::V + (i % NS) * C::TILE);
-                mma_commit(&bar[C::dp_full]);
-                mma_commit(&bar[C::v_empty + i % NS]);
+                mma_nt<D>(tmem + C::tP, sm + C::O, sm + C::V + (i % NV) * C::TILE);
+                commit(&bar[C::dp_full]);
+                commit(&bar[C::v_empty + i % NV]);
             };
             w.wait(&bar[C::q_full], 0);
             scores(0);
             dprobs(0);
-            for (int i = 0; i < steps && !w.aborted(); ++i) {
+            for (int i = 0; i < steps && !w.stopped(); ++i) {
                 if (i + 1 < steps) {
                     if (i > 0) w.wait(&bar[C::dq_done + ((i + 1) & 1)], (i - 1) >> 1);
                     scores(i + 1);
@@ -199,16 +206,16 @@ __global__ void __launch_bounds__(NTH, 1)
                     dprobs(i + 1);
                 }
                 w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
-                if (w.aborted()) break;
+                if (w.stopped()) break;
                 tc_fence_after();
                 if (i >= steps - n)
-                    mma_chunks<D>(tmem + C::tQ, tmem + C::tS + 128 * (i & 1), sm + C::K + (i % NS) * C::TILE, 0, 8,
+                    mma_chunks<D>(tmem + C::tQ, tmem + C::tS + 128 * (i & 1), sm + C::K + (i % NK) * C::TILE, 0, 8,
                                   i > steps - n);
-                mma_commit(&bar[C::dq_done + (i & 1)]);
-                mma_commit(&bar[C::k_empty + i % NS]);
+                commit(&bar[C::dq_done + (i & 1)]);
+                commit(&bar[C::k_empty + i % NK]);
             }
-            if (w.aborted()) {
-                mma_commit(&bar[C::drain]);
+            if (w.stopped()) {
+                commit(&bar[C::drain]);
                 mbar_wait_bounded(&bar[C::drain], 0, 100000000ull);
             }
         }
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(NTH, 1)
             tmem_ld32(tP + 32, dp[1]);
             tmem_wait_ld();
             tc_fence_before();
-            arrive(&bar[C::dp_free]);
+            warp_arrive(&bar[C::dp_free], lane);
             if (i < steps - n) {
                 uint64_t acc = 0;
 #pragma unroll
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 tmem_wait_st();
             }
             tc_fence_before();
-            arrive(&bar[C::ds_full + (i & 1)]);
+            warp_arrive(&bar[C::ds_full + (i & 1)], lane);
         }
         if (!joined) named_bar(1, NEL);  // left early: the other warps still come by
         if (!w.stopped()) {
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(NTH, 1)
                               rows);
         }
     }
-    if (w.aborted() && warp == 9 && lane == 0) drain_loads(bar, C::q_full, 1 + 2 * NS);
+    if (w.aborted() && warp == 9 && lane == 0) drain_loads(bar, C::q_full, 1 + NK + NV);
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {
@@ -388,7 +395,7 @@ __global__ void __launch_bounds__(NTH, 1)
         for (int i = 0; i < C::NBAR; ++i) {
             int c = 1;
             if (i >= C::q_full && i < C::o_full) c = 1 + 32;
-            if ((i >= C::p_half && i < C::ds_full) || i == C::ds_full) c = NEL;
+            if ((i >= C::p_half && i < C::ds_full) || i == C::ds_full) c = NEL / 32;  // one a warp
             mbar_init(&bar[i], c);
         }
         fence_mbar_init();
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(NTH, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp == 9) {
         if (lane == 0) {
@@ -441,54 +448,56 @@ __global__ void __launch_bounds__(NTH, 1)
             __syncwarp();
         }
     } else if (warp == 8) {
-        if (lane == 0) {
+        {
             auto arrived = [&](int first, int i) {
                 w.wait(&bar[first + i % NS], i / NS);
                 if (tail < BT) w.wait(&bar[C::zeroed + i % NS], i / NS);
             };
             auto scores = [&](int i) {
                 arrived(C::q_full, i);
-                if (w.aborted()) return;
+                if (w.stopped()) return;
                 tc_fence_after();
                 mma_nt<D>(tmem + C::tS, sm + C::K, sm + C::Q + (i % NS) * C::TILE);
-                mma_commit(&bar[C::s_full]);
+                commit(&bar[C::s_full]);
             };
             auto dprobs = [&](int i) {
                 arrived(C::o_full, i);
-                if (w.aborted()) return;
+                if (w.stopped()) return;
                 tc_fence_after();
                 mma_nt<D>(tmem + C::tP, sm + C::V, sm + C::O + (i % NS) * C::TILE);
-                mma_commit(&bar[C::dp_full]);
+                commit(&bar[C::dp_full]);
             };
             w.wait(&bar[C::kv_full], 0);
             scores(0);
             dprobs(0);
-            for (int i = 0; i < steps && !w.aborted(); ++i) {
+            for (int i = 0; i < steps && !w.stopped(); ++i) {
                 const unsigned char *q = sm + C::Q + (i % NS) * C::TILE, *o = sm + C::O + (i % NS) * C::TILE;
                 w.wait(&bar[C::p_half], i);
-                if (w.aborted()) break;
+                if (w.stopped()) break;
                 tc_fence_after();
                 mma_chunks<D>(tmem + C::tV, tmem + C::tS, o, 0, 4, i > 0);
                 w.wait(&bar[C::p_half + 1], i);
-                if (w.aborted()) break;
+                if (w.stopped()) break;
                 tc_fence_after();
                 mma_chunks<D>(tmem + C::tV, tmem + C::tS, o, 4, 8, true);
-                mma_commit(&bar[C::dv_done]);
-                w.wait(&bar[C::ds_full], i);
-                if (w.aborted()) break;
-                tc_fence_after();
-                mma_chunks<D>(tmem + C::tK, tmem + C::tP, q, 0, 8, i > 0);
-                mma_commit(&bar[C::dk_done]);
-                mma_commit(&bar[C::empty + i % NS]);
-                if (i + 1 < steps) {
+                commit(&bar[C::dv_done]);
+                if (i + 1 < steps) {  // over P^T; it runs while dS^T is formed
                     w.wait(&bar[C::dv_done], i);
                     scores(i + 1);
+                }
+                w.wait(&bar[C::ds_full], i);
+                if (w.stopped()) break;
+                tc_fence_after();
+                mma_chunks<D>(tmem + C::tK, tmem + C::tP, q, 0, 8, i > 0);
+                commit(&bar[C::dk_done]);
+                commit(&bar[C::empty + i % NS]);
+                if (i + 1 < steps) {  // over dS^T; it runs while the next P^T is formed
                     w.wait(&bar[C::dk_done], i);
                     dprobs(i + 1);
                 }
             }
-            if (w.aborted()) {
-                mma_commit(&bar[C::drain]);
+            if (w.stopped()) {
+                commit(&bar[C::drain]);
                 mbar_wait_bounded(&bar[C::drain], 0, 100000000ull);
             }
         }
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 tmem_st16(tS + c0, pk);
                 tmem_wait_st();
                 tc_fence_before();
-                arrive(&bar[C::p_half + q]);
+                warp_arrive(&bar[C::p_half + q], lane);
             }
             w.wait(&bar[C::dp_full], i);
             if (w.stopped()) break;
@@ -555,7 +564,7 @@ __global__ void __launch_bounds__(NTH, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            arrive(&bar[C::ds_full]);
+            warp_arrive(&bar[C::ds_full], lane);
         }
         if (!w.stopped()) {
             w.wait(&bar[C::dk_done], steps - 1);
