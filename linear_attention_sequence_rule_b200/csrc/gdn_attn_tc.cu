@@ -134,7 +134,6 @@ __global__ void __launch_bounds__(NTH, 1)
             auto scores = [&](int j) {
                 const int s = j % NS;
                 w.wait(&bar[C::k_full + s], j / NS);
-                if (w.stopped()) return;
                 tc_fence_after();
                 mma_nt<D>(tS, qt, sm + C::K + s * C::TILE);
                 commit(&bar[C::s_full + t]);
@@ -151,11 +150,9 @@ __global__ void __launch_bounds__(NTH, 1)
                 w.wait(&bar[C::v_full + s], j / NS);
                 if (j == nmax - 1 && at.len < nmax * BT) w.wait(&bar[C::v_zeroed], 0);
                 w.wait(&bar[C::p_half + 2 * t], j);
-                if (w.stopped()) break;
                 tc_fence_after();
                 mma_tn<D>(tO, tP, sm + C::V + s * C::TILE, 0, 4, j > 0);
                 w.wait(&bar[C::p_half + 2 * t + 1], j);
-                if (w.stopped()) break;
                 tc_fence_after();
                 mma_tn<D>(tO, tP, sm + C::V + s * C::TILE, 4, 8, true);
                 commit(&bar[C::pv_done + t]);
@@ -214,7 +211,6 @@ __global__ void __launch_bounds__(NTH, 1)
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             if (C::SEP && j > 0) {  // O is at rest, and the last P has been read
                 w.wait(&bar[C::pv_done + t], j - 1);
-                if (w.stopped()) break;
                 tc_fence_after();
             }
             const bool move = (top - m) * scale2 > 8.f;  // also from -inf

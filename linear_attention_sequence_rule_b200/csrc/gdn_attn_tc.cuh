@@ -21,25 +21,26 @@ constexpr int BT = 128;               // rows of every tile (queries or keys)
 constexpr int kSub = BT * 128;        // bytes of a 64-column sub-tile: 128 rows of 128 bytes, swizzled
 
 // Barriers with bounded waits: a wait that runs out records it and raises the CTA's abort flag, after
-// which no wait waits and no role issues work.
+// which no wait waits and every role ends with its current step.  A wait that finds its phase complete
+// costs one probe: between batches of products the issuing warp's own latency leaves the tensor pipe
+// idle (its queue holds a few instructions), so the flag is looked at once a step and in waits that wait.
 struct Waits {
     int *abort, *error;
-    __device__ __forceinline__ void slow(uint64_t *b, uint32_t parity) const
-    {
-        if (!mbar_wait_bounded(b, parity, kWaitNs)) {
-            atomicOr(error, 1);
-            *(volatile int *)abort = 1;
-        }
-    }
-    __device__ __forceinline__ void wait(uint64_t *b, int phase) const
-    {
-        if (*(volatile int *)abort) return;
-        if (mbar_try_wait(b, phase & 1)) return;
-        slow(b, phase & 1);
-    }
     __device__ __forceinline__ bool aborted() const { return *(volatile int *)abort != 0; }
     // the same for a whole warp, so that its lanes leave a loop together
     __device__ __forceinline__ bool stopped() const { return __any_sync(0xffffffffu, aborted()); }
+    __device__ __forceinline__ void wait(uint64_t *b, int phase) const
+    {
+        if (mbar_try_wait(b, phase & 1)) return;
+        const uint64_t t0 = globaltimer_ns();
+        while (!aborted()) {
+            if (mbar_try_wait(b, phase & 1)) return;
+            if (globaltimer_ns() - t0 > kWaitNs) {
+                atomicOr(error, 1);
+                *(volatile int *)abort = 1;
+            }
+        }
+    }
 };
 
 __device__ __forceinline__ void arrive(uint64_t *b)

@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(NTH, 1)
             auto scores = [&](int i) {
                 w.wait(&bar[C::k_full + i % NK], i / NK);
                 if (rows < BT) w.wait(&bar[C::k_zeroed + i % NK], i / NK);
-                if (w.stopped()) return;
                 tc_fence_after();
                 mma_nt<D>(tmem + C::tS + 128 * (i & 1), sm + C::Q, sm + C::K + (i % NK) * C::TILE);
                 commit(&bar[C::s_full + (i & 1)]);
@@ -189,7 +188,6 @@ __global__ void __launch_bounds__(NTH, 1)
             auto dprobs = [&](int i) {
                 w.wait(&bar[C::v_full + i % NV], i / NV);
                 if (rows < BT) w.wait(&bar[C::v_zeroed + i % NV], i / NV);
-                if (w.stopped()) return;
                 tc_fence_after();
                 mma_nt<D>(tmem + C::tP, sm + C::O, sm + C::V + (i % NV) * C::TILE);
                 commit(&bar[C::dp_full]);
@@ -206,7 +204,6 @@ __global__ void __launch_bounds__(NTH, 1)
                     dprobs(i + 1);
                 }
                 w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
-                if (w.stopped()) break;
                 tc_fence_after();
                 if (i >= steps - n)
                     mma_chunks<D>(tmem + C::tQ, tmem + C::tS + 128 * (i & 1), sm + C::K + (i % NK) * C::TILE, 0, 8,
@@ -286,7 +283,6 @@ __global__ void __launch_bounds__(NTH, 1)
             }
             float dp[2][32];
             w.wait(&bar[C::dp_full], i);
-            if (w.stopped()) break;
             tc_fence_after();
             tmem_ld32(tP, dp[0]);
             tmem_ld32(tP + 32, dp[1]);
@@ -455,14 +451,12 @@ __global__ void __launch_bounds__(NTH, 1)
             };
             auto scores = [&](int i) {
                 arrived(C::q_full, i);
-                if (w.stopped()) return;
                 tc_fence_after();
                 mma_nt<D>(tmem + C::tS, sm + C::K, sm + C::Q + (i % NS) * C::TILE);
                 commit(&bar[C::s_full]);
             };
             auto dprobs = [&](int i) {
                 arrived(C::o_full, i);
-                if (w.stopped()) return;
                 tc_fence_after();
                 mma_nt<D>(tmem + C::tP, sm + C::V, sm + C::O + (i % NS) * C::TILE);
                 commit(&bar[C::dp_full]);
@@ -473,11 +467,9 @@ __global__ void __launch_bounds__(NTH, 1)
             for (int i = 0; i < steps && !w.stopped(); ++i) {
                 const unsigned char *q = sm + C::Q + (i % NS) * C::TILE, *o = sm + C::O + (i % NS) * C::TILE;
                 w.wait(&bar[C::p_half], i);
-                if (w.stopped()) break;
                 tc_fence_after();
                 mma_chunks<D>(tmem + C::tV, tmem + C::tS, o, 0, 4, i > 0);
                 w.wait(&bar[C::p_half + 1], i);
-                if (w.stopped()) break;
                 tc_fence_after();
                 mma_chunks<D>(tmem + C::tV, tmem + C::tS, o, 4, 8, true);
                 commit(&bar[C::dv_done]);
@@ -486,7 +478,6 @@ __global__ void __launch_bounds__(NTH, 1)
                     scores(i + 1);
                 }
                 w.wait(&bar[C::ds_full], i);
-                if (w.stopped()) break;
                 tc_fence_after();
                 mma_chunks<D>(tmem + C::tK, tmem + C::tP, q, 0, 8, i > 0);
                 commit(&bar[C::dk_done]);
@@ -542,7 +533,6 @@ __global__ void __launch_bounds__(NTH, 1)
                 warp_arrive(&bar[C::p_half + q], lane);
             }
             w.wait(&bar[C::dp_full], i);
-            if (w.stopped()) break;
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
