@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(NTH, 1)
             tc_fence_after();
             if (!w.stopped()) {
                 const int64_t row0 = at.t0 + q0 + t * BT;
-                store_rows<D>(tO, 1.f / l, sm + C::Q + t * C::TILE, wq, lane, out + (row0 * Hq + h) * D, (int64_t)Hq * D,
+                store_rows<D, D>(tO, 1.f / l, sm + C::Q + t * C::TILE, wq, lane, 0, out + (row0 * Hq + h) * D, (int64_t)Hq * D,
                               rows - t * BT);
                 if (lse && r < rows - t * BT) lse[(row0 + r) * Hq + h] = fmaf(m, scale2, log2f(l)) * kLn2;
             }

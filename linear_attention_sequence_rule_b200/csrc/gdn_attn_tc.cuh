@@ -29,12 +29,25 @@ struct Waits {
     __device__ __forceinline__ bool aborted() const { return *(volatile int *)abort != 0; }
     // the same for a whole warp, so that its lanes leave a loop together
     __device__ __forceinline__ bool stopped() const { return __any_sync(0xffffffffu, aborted()); }
+    // (without a time of its own the probe sleeps for what the hardware sees fit, and wakes sooner)
+    __device__ __forceinline__ static bool over(uint64_t *b, uint32_t parity)
+    {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(b)), "r"(parity)
+            : "memory");
+        return ok != 0;
+    }
     __device__ __forceinline__ void wait(uint64_t *b, int phase) const
     {
-        if (mbar_try_wait(b, phase & 1)) return;
+        if (over(b, phase & 1)) return;
         const uint64_t t0 = globaltimer_ns();
         while (!aborted()) {
-            if (mbar_try_wait(b, phase & 1)) return;
+            if (over(b, phase & 1)) return;
             if (globaltimer_ns() - t0 > kWaitNs) {
                 atomicOr(error, 1);
                 *(volatile int *)abort = 1;
@@ -145,10 +158,10 @@ __device__ __forceinline__ void commit(uint64_t *bar)
         : "memory");
 }
 
-// D[128 x 128] = A B^T over the head size: both tiles K-major in shared memory
-template <int D> __device__ __forceinline__ void mma_nt(uint32_t d, const unsigned char *a, const unsigned char *b)
+// D[128 x N] = A B^T over the head size: both tiles K-major in shared memory (b: the first of N rows)
+template <int D, int N = BT> __device__ __forceinline__ void mma_nt(uint32_t d, const unsigned char *a, const unsigned char *b)
 {
-    constexpr uint32_t id = idesc_bf16(BT, BT, 0, 0);
+    constexpr uint32_t id = idesc_bf16(BT, N, 0, 0);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t o = (kk >> 2) * kSub + (kk & 3) * 32;
@@ -167,19 +180,19 @@ __device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, const unsigned ch
         mma_ts(d, a + 8 * kk, sdesc_sw128(smem_u32(b) + kk * 2048, kSub, 1024), id, accumulate || kk > k0);
 }
 
-// 32 fp32 accumulator rows (thread = row of its warp's 32; columns of `acc` at tensor memory address t)
-// scaled and written as bf16 rows: through the warp's own rows of `buf` (D * 2 bytes a row, 16-byte
-// units XORed with the row), then in whole rows to g + row * ld for rows below n.
-template <int D>
-__device__ __forceinline__ void store_rows(uint32_t t, float f, unsigned char *buf, int warp, int lane, __nv_bfloat16 *g,
-                                           int64_t ld, int n)
+// NC columns from column c0 on of an accumulator (tensor memory address t of column 0; thread = row of
+// its warp's 32), scaled and written as bf16: through the warp's own rows of `buf` (D * 2 bytes a row,
+// 16-byte units XORed with the row), then in whole row parts to g + row * ld for rows below n.
+template <int D, int NC>
+__device__ __forceinline__ void store_rows(uint32_t t, float f, unsigned char *buf, int warp, int lane, int c0,
+                                           __nv_bfloat16 *g, int64_t ld, int n)
 {
-    constexpr int UN = D / 8;  // 16-byte units a row
-    const int r = 32 * warp + lane;
+    constexpr int UN = NC / 8;  // 16-byte units a row
+    const int r = 32 * warp + lane, u0 = c0 / 8;
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) {
+    for (int x = 0; x < NC / 32; ++x) {
         float o[32];
-        tmem_ld32(t + 32 * x, o);
+        tmem_ld32(t + c0 + 32 * x, o);
         tmem_wait_ld();
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -188,18 +201,17 @@ __device__ __forceinline__ void store_rows(uint32_t t, float f, unsigned char *b
             w.y = pack_bf16x2(o[8 * u + 2] * f, o[8 * u + 3] * f);
             w.z = pack_bf16x2(o[8 * u + 4] * f, o[8 * u + 5] * f);
             w.w = pack_bf16x2(o[8 * u + 6] * f, o[8 * u + 7] * f);
-            *reinterpret_cast<uint4 *>(buf + r * (2 * D) + (((4 * x + u) ^ (r & 7)) << 4)) = w;
+            *reinterpret_cast<uint4 *>(buf + r * (2 * D) + (((u0 + 4 * x + u) ^ (r & 7)) << 4)) = w;
         }
     }
     __syncwarp();
 #pragma unroll 4
     for (int i = lane; i < 32 * UN; i += 32) {
-        const int rr = 32 * warp + i / UN, u = i % UN;
+        const int rr = 32 * warp + i / UN, u = u0 + i % UN;
         if (rr < n)
             *reinterpret_cast<uint4 *>(g + (int64_t)rr * ld + 8 * u) =
                 *reinterpret_cast<const uint4 *>(buf + rr * (2 * D) + ((u ^ (rr & 7)) << 4));
     }
-    __syncwarp();
 }
 
 // 3-D view [tokens][heads][d] of a bf16 tensor; box = 64 features x 1 head x 128 tokens, 128-byte swizzle

@@ -16,10 +16,17 @@
 // average over more keys, and D is taken from out.  The query side writes D and -lse log2 e for
 // the key side, head by head ([Hq][tokens] each), into the workspace.
 //
-// In both kernels warps 0-7 work element by element (a thread has a row; two groups of 4 warps take
-// different 32-column chunks), warp 8 issues the products, warp 9 loads.  P and dS (bf16)
-// are written over the first half of the very S or dP columns they came from, which their own
-// thread has read.
+// Both kernels work in steps of 64 keys (query side) or 64 queries (key side): 128 x 64 tiles of S and
+// dP, two of each in tensor memory beside the gradients (2 x 64 + 2 x 64 + 256 columns at d = 128), so
+// that the products of one step run while the other's elements are worked on.  Steps of 128 with one
+// dP (or, on the key side, one S) buffer spend half their time in the chain of waits between products
+// and elements (about 1900 cycles a step with products and exponentials taken out); a product 64 wide
+// takes 48 cycles for 32 cycles' work (both operands come from shared memory), and is still faster.
+//   warps 0-7, 8-15  element by element, the even and the odd steps: a thread has a row, 32 columns
+//   warps 16-18      issue the products
+//   warp 19          loads; zeroes rows behind the sequence's end
+// P and dS (bf16) are written over the first half of the very S or dP columns they came from, which
+// their own thread has read.
 #include <math.h>
 
 #include "gdn_attn_tc.cuh"
@@ -34,19 +41,22 @@ namespace {
 
 using namespace attn;
 
-constexpr int NTH = 320;
-constexpr int NEL = 256;         // threads of the element-wise warps
+constexpr int NTH = 640;
+constexpr int NEL = 512;         // threads of the element-wise warps
+constexpr int HT = 64;           // rows of the other side a step
+constexpr int kHalf = HT * 128;  // bytes from a tile's first half to its second (in each sub-tile)
 constexpr int kExactBlocks = 2;
 
-// D[128 x D] (+)= A B with A's chunks of 32 columns (16 of tensor memory) 32 apart: k steps k0 .. k1 - 1
+// D[128 x D] (+)= A B over a step's 64 rows of B: A (bf16) in two chunks of 32 columns (16 of tensor
+// memory) that lie 32 apart
 template <int D>
-__device__ __forceinline__ void mma_chunks(uint32_t d, uint32_t a, const unsigned char *b, int k0, int k1, bool accumulate)
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, const unsigned char *b, bool accumulate)
 {
     constexpr uint32_t id = idesc_bf16(BT, D, 0, 1);
 #pragma unroll
-    for (int kk = k0; kk < k1; ++kk)
+    for (int kk = 0; kk < 4; ++kk)
         mma_ts(d, a + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_sw128(smem_u32(b) + kk * 2048, kSub, 1024), id,
-                    accumulate || kk > k0);
+               accumulate || kk > 0);
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&v)[16])
@@ -85,15 +95,17 @@ template <int D> struct DqCfg {
     static constexpr int k_zeroed = v_empty + NV;  // [NK] the stage has no row behind the end (ragged ends only)
     static constexpr int v_zeroed = k_zeroed + NK; // [NV]
     static constexpr int s_full = v_zeroed + NV;   // [2]
-    static constexpr int dp_full = s_full + 2;
-    static constexpr int dp_free = dp_full + 1;    // dP has been read
-    static constexpr int ds_full = dp_free + 1;    // [2] dS is there (first pass: S has been read)
+    static constexpr int dp_full = s_full + 2;     // [2]
+    static constexpr int dp_free = dp_full + 2;    // [2] dP has been read
+    static constexpr int ds_full = dp_free + 2;    // [2] dS is there (first pass: S has been read)
     static constexpr int dq_done = ds_full + 2;    // [2] dS has been used
-    static constexpr int drain = dq_done + 2;
-    static constexpr int NBAR = drain + 1;
+    static constexpr int all_done = dq_done + 2;   // dQ is there (a barrier of one phase: a warp that
+                                                   // passes over phases cannot tell them by parity)
+    static constexpr int drain = all_done + 1;     // [3]
+    static constexpr int NBAR = drain + 3;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
-    static constexpr uint32_t tS = 0, tP = 256, tQ = 384;  // S[2], dP, dQ
+    static constexpr uint32_t tS = 0, tP = 128, tQ = 256;  // S[2], dP[2], dQ
     static_assert(TOTAL <= 232448, "shared memory budget");
 };
 
@@ -119,19 +131,20 @@ __global__ void __launch_bounds__(NTH, 1)
     const AttnTile at = attn_tile(cu, B, T, BT, blockIdx.x / Hq);
     if (at.seq < 0) return;
     const int h = blockIdx.x % Hq, hk = h / (Hq / Hk);
-    const int n = at.block + 1;                    // key blocks
-    const bool exact = at.block < kExactBlocks;
-    const int steps = exact ? 2 * n : n;           // the first n form D
     const int rows = at.len - at.block * BT;       // that exist
+    const int n = (min(at.len, (at.block + 1) * BT) + HT - 1) / HT;  // steps of a pass
+    const int nt = (n + 1) / 2;                    // key tiles of a pass
+    const bool exact = at.block < kExactBlocks;
+    const int passes = exact ? 2 : 1, steps = passes * n;  // the first of two passes forms D
     const int64_t row0 = at.t0 + at.block * BT;
 
     if (tid == 0) {
         for (int i = 0; i < C::NBAR; ++i)
-            mbar_init(&bar[i], i == C::dp_free || (i >= C::ds_full && i < C::dq_done) ? NEL / 32 : 1);  // one a warp
+            mbar_init(&bar[i], i >= C::dp_free && i < C::dq_done ? NEL / 64 : 1);  // one a warp
         fence_mbar_init();
         *abort_flag = 0;
     }
-    if (warp == 9) {
+    if (warp == 19) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -140,95 +153,103 @@ __global__ void __launch_bounds__(NTH, 1)
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-    if (warp == 9) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&bar[C::q_full], 2 * C::TILE);
-            load_tile<D>(sm + C::Q, &tmQ, &bar[C::q_full], h, (int)row0);
-            load_tile<D>(sm + C::O, &tmO, &bar[C::q_full], h, (int)row0);
-        }
-        for (int i = 0; i < steps; ++i) {
-            const int sk = i % NK, sv = i % NV, j = i % n;
+    // registers: 640 x 96 = 61440 at launch; 128 x 56 + 512 x 104 = 60416 after the two roles' changes
+    if (warp >= 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 19) {
             if (lane == 0) {
-                if (i >= NK) w.wait(&bar[C::k_empty + sk], i / NK - 1);
-                if (!w.aborted()) {
-                    mbar_arrive_expect_tx(&bar[C::k_full + sk], C::TILE);
-                    load_tile<D>(sm + C::K + sk * C::TILE, &tmK, &bar[C::k_full + sk], hk, (int)at.t0 + j * BT);
-                }
-                if (i >= NV) w.wait(&bar[C::v_empty + sv], i / NV - 1);
-                if (!w.aborted()) {
-                    mbar_arrive_expect_tx(&bar[C::v_full + sv], C::TILE);
-                    load_tile<D>(sm + C::V + sv * C::TILE, &tmV, &bar[C::v_full + sv], hk, (int)at.t0 + j * BT);
-                }
+                mbar_arrive_expect_tx(&bar[C::q_full], 2 * C::TILE);
+                load_tile<D>(sm + C::Q, &tmQ, &bar[C::q_full], h, (int)row0);
+                load_tile<D>(sm + C::O, &tmO, &bar[C::q_full], h, (int)row0);
             }
-            __syncwarp();
-            if (w.stopped()) break;
-            if (rows < BT) {
-                if (j == n - 1) {
-                    w.wait(&bar[C::k_full + sk], i / NK);
-                    w.wait(&bar[C::v_full + sv], i / NV);
-                    if (w.stopped()) break;
-                    zero_rows<D>(sm + C::K + sk * C::TILE, rows, lane);
-                    zero_rows<D>(sm + C::V + sv * C::TILE, rows, lane);
-                }
+            for (int i = 0; i < passes * nt; ++i) {
+                const int sk = i % NK, sv = i % NV, j = i % nt;
                 if (lane == 0) {
-                    arrive(&bar[C::k_zeroed + sk]);
-                    arrive(&bar[C::v_zeroed + sv]);
+                    if (i >= NK) w.wait(&bar[C::k_empty + sk], i / NK - 1);
+                    if (!w.aborted()) {
+                        mbar_arrive_expect_tx(&bar[C::k_full + sk], C::TILE);
+                        load_tile<D>(sm + C::K + sk * C::TILE, &tmK, &bar[C::k_full + sk], hk, (int)at.t0 + j * BT);
+                    }
+                    if (i >= NV) w.wait(&bar[C::v_empty + sv], i / NV - 1);
+                    if (!w.aborted()) {
+                        mbar_arrive_expect_tx(&bar[C::v_full + sv], C::TILE);
+                        load_tile<D>(sm + C::V + sv * C::TILE, &tmV, &bar[C::v_full + sv], hk, (int)at.t0 + j * BT);
+                    }
+                }
+                __syncwarp();
+                if (w.stopped()) break;
+                if (rows < BT) {
+                    if (j == nt - 1) {
+                        w.wait(&bar[C::k_full + sk], i / NK);
+                        w.wait(&bar[C::v_full + sv], i / NV);
+                        if (w.stopped()) break;
+                        zero_rows<D>(sm + C::K + sk * C::TILE, rows, lane);
+                        zero_rows<D>(sm + C::V + sv * C::TILE, rows, lane);
+                    }
+                    if (lane == 0) {
+                        arrive(&bar[C::k_zeroed + sk]);
+                        arrive(&bar[C::v_zeroed + sv]);
+                    }
                 }
             }
-        }
-    } else if (warp == 8) {
-        {
-            auto scores = [&](int i) {
-                w.wait(&bar[C::k_full + i % NK], i / NK);
-                if (rows < BT) w.wait(&bar[C::k_zeroed + i % NK], i / NK);
-                tc_fence_after();
-                mma_nt<D>(tmem + C::tS + 128 * (i & 1), sm + C::Q, sm + C::K + (i % NK) * C::TILE);
-                commit(&bar[C::s_full + (i & 1)]);
-            };
-            auto dprobs = [&](int i) {
-                w.wait(&bar[C::v_full + i % NV], i / NV);
-                if (rows < BT) w.wait(&bar[C::v_zeroed + i % NV], i / NV);
-                tc_fence_after();
-                mma_nt<D>(tmem + C::tP, sm + C::O, sm + C::V + (i % NV) * C::TILE);
-                commit(&bar[C::dp_full]);
-                commit(&bar[C::v_empty + i % NV]);
-            };
+        } else if (warp == 16) {  // S
             w.wait(&bar[C::q_full], 0);
-            scores(0);
-            dprobs(0);
-            for (int i = 0; i < steps && !w.stopped(); ++i) {
-                if (i + 1 < steps) {
-                    if (i > 0) w.wait(&bar[C::dq_done + ((i + 1) & 1)], (i - 1) >> 1);
-                    scores(i + 1);
-                    w.wait(&bar[C::dp_free], i);
-                    dprobs(i + 1);
+            for (int p = 0, i = 0; p < passes; ++p)
+                for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
+                    const int j = p * nt + (s >> 1);
+                    if (i > 1) w.wait(&bar[C::dq_done + (i & 1)], (i >> 1) - 1);
+                    w.wait(&bar[C::k_full + j % NK], j / NK);
+                    if (rows < BT) w.wait(&bar[C::k_zeroed + j % NK], j / NK);
+                    tc_fence_after();
+                    mma_nt<D, HT>(tmem + C::tS + HT * (i & 1), sm + C::Q, sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf);
+                    commit(&bar[C::s_full + (i & 1)]);
                 }
-                w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
-                tc_fence_after();
-                if (i >= steps - n)
-                    mma_chunks<D>(tmem + C::tQ, tmem + C::tS + 128 * (i & 1), sm + C::K + (i % NK) * C::TILE, 0, 8,
-                                  i > steps - n);
-                commit(&bar[C::dq_done + (i & 1)]);
-                commit(&bar[C::k_empty + i % NK]);
-            }
-            if (w.stopped()) {
-                commit(&bar[C::drain]);
-                mbar_wait_bounded(&bar[C::drain], 0, 100000000ull);
-            }
+        } else if (warp == 17) {  // dP
+            w.wait(&bar[C::q_full], 0);
+            for (int p = 0, i = 0; p < passes; ++p)
+                for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
+                    const int j = p * nt + (s >> 1);
+                    if (i > 1) w.wait(&bar[C::dp_free + (i & 1)], (i >> 1) - 1);
+                    w.wait(&bar[C::v_full + j % NV], j / NV);
+                    if (rows < BT) w.wait(&bar[C::v_zeroed + j % NV], j / NV);
+                    tc_fence_after();
+                    mma_nt<D, HT>(tmem + C::tP + HT * (i & 1), sm + C::O, sm + C::V + (j % NV) * C::TILE + (s & 1) * kHalf);
+                    commit(&bar[C::dp_full + (i & 1)]);
+                    if ((s & 1) || s == n - 1) commit(&bar[C::v_empty + j % NV]);
+                }
+        } else {  // dQ
+            for (int p = 0, i = 0; p < passes; ++p)
+                for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
+                    const int j = p * nt + (s >> 1);
+                    w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
+                    tc_fence_after();
+                    if (p == passes - 1)
+                        mma_step<D>(tmem + C::tQ, tmem + C::tS + HT * (i & 1),
+                                    sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf, s > 0);
+                    commit(&bar[C::dq_done + (i & 1)]);
+                    if ((s & 1) || s == n - 1) commit(&bar[C::k_empty + j % NK]);
+                }
+            commit(&bar[C::all_done]);
+        }
+        if (warp < 19 && w.stopped()) {  // products issued already end before the tensor memory is freed
+            commit(&bar[C::drain + warp - 16]);
+            mbar_wait_bounded(&bar[C::drain + warp - 16], 0, 100000000ull);
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int g = warp >> 2, wq = warp & 3, r = tid & (BT - 1);
+        const int set = g >> 1, c0 = 32 * (g & 1);  // steps of this parity, these columns
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const bool live = r < rows;
         const float nl = live ? -lse[(row0 + r) * Hq + h] * kLog2e : 0.f;
         float nd = 0.f;
-        if (!exact) {  // D from out: this thread's half of the row
+        if (!exact) {  // D from out: this thread's quarter of the row
             w.wait(&bar[C::q_full], 0);
             if (live) {
-                const uint4 *o = reinterpret_cast<const uint4 *>(out + ((row0 + r) * Hq + h) * D) + g * (D / 16);
+                const uint4 *o = reinterpret_cast<const uint4 *>(out + ((row0 + r) * Hq + h) * D) + g * (D / 32);
 #pragma unroll
-                for (int u = 0; u < D / 16; ++u) {
-                    const int x = g * (D / 16) + u;
+                for (int u = 0; u < D / 32; ++u) {
+                    const int x = g * (D / 32) + u;
                     const uint4 a = o[u], b = *reinterpret_cast<const uint4 *>(sm + C::O + (x >> 3) * kSub + r * 128 +
                                                                                (((x & 7) ^ (r & 7)) << 4));
                     const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
@@ -240,8 +261,10 @@ __global__ void __launch_bounds__(NTH, 1)
                 }
             }
         }
-        auto join = [&]() {  // the two halves of D; for the key side too
-            red[g * BT + r] = nd;
+        auto join = [&]() {  // the four parts of D; for the key side too
+            if (g >= 2) red[(g - 2) * BT + r] = nd;
+            named_bar(1, NEL);
+            if (g < 2) red[g * BT + r] += nd;
             named_bar(1, NEL);
             nd = red[r] + red[BT + r];
             if (g == 0 && live) {
@@ -252,83 +275,72 @@ __global__ void __launch_bounds__(NTH, 1)
         bool joined = !exact;
         if (joined) join();
         const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e), nl2 = pack2(nl, nl);
-        for (int i = 0; i < steps; ++i) {
-            if (!joined && i == n) {
+        const uint32_t tS = tmem + lanes + C::tS + HT * set + c0, tP = tmem + lanes + C::tP + HT * set + c0;
+        for (int i = set; i < steps; i += 2) {
+            if (!joined && i >= n) {
                 join();
                 joined = true;
             }
             const uint64_t nd2 = pack2(nd, nd);
-            const uint32_t tS = tmem + lanes + C::tS + 128 * (i & 1) + 64 * g, tP = tmem + lanes + C::tP + 64 * g;
-            float s[2][32];
+            const int key0 = (i % n) * HT + c0 - at.block * BT;  // of this thread's columns, as r counts
+            float s[32];
             w.wait(&bar[C::s_full + (i & 1)], i >> 1);
             if (w.stopped()) break;
             tc_fence_after();
-            tmem_ld32(tS, s[0]);
-            tmem_ld32(tS + 32, s[1]);
+            tmem_ld32(tS, s);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                    unpack2(fma2(pack2(s[q][x], s[q][x + 1]), sc2, nl2), s[q][x], s[q][x + 1]);
-                    s[q][x] = ex2_approx(s[q][x]);
-                    s[q][x + 1] = ex2_approx(s[q][x + 1]);
-                }
-            if (i % n == n - 1) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (64 * g + 32 * q + x > r) s[q][x] = 0.f;
+            for (int x = 0; x < 32; x += 2) {
+                unpack2(fma2(pack2(s[x], s[x + 1]), sc2, nl2), s[x], s[x + 1]);
+                s[x] = ex2_approx(s[x]);
+                s[x + 1] = ex2_approx(s[x + 1]);
             }
-            float dp[2][32];
-            w.wait(&bar[C::dp_full], i);
+            if (key0 >= 0) {  // the diagonal block
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    if (key0 + x > r) s[x] = 0.f;
+            }
+            float dp[32];
+            w.wait(&bar[C::dp_full + (i & 1)], i >> 1);
             tc_fence_after();
-            tmem_ld32(tP, dp[0]);
-            tmem_ld32(tP + 32, dp[1]);
+            tmem_ld32(tP, dp);
             tmem_wait_ld();
             tc_fence_before();
-            warp_arrive(&bar[C::dp_free], lane);
-            if (i < steps - n) {
+            warp_arrive(&bar[C::dp_free + (i & 1)], lane);
+            if (exact && i < n) {
                 uint64_t acc = 0;
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2)
-                        acc = fma2(pack2(s[q][x], s[q][x + 1]), pack2(dp[q][x], dp[q][x + 1]), acc);
+                for (int x = 0; x < 32; x += 2) acc = fma2(pack2(s[x], s[x + 1]), pack2(dp[x], dp[x + 1]), acc);
                 float a, b;
                 unpack2(acc, a, b);
                 nd -= a + b;
             } else {
+                uint32_t ds[16];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t ds[16];
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                        float a, b;
-                        unpack2(mul2(pack2(s[q][x], s[q][x + 1]), add2(pack2(dp[q][x], dp[q][x + 1]), nd2)), a, b);
-                        ds[x >> 1] = pack_bf16x2(a, b);
-                    }
-                    tmem_st16(tS + 32 * q, ds);
+                for (int x = 0; x < 32; x += 2) {
+                    float a, b;
+                    unpack2(mul2(pack2(s[x], s[x + 1]), add2(pack2(dp[x], dp[x + 1]), nd2)), a, b);
+                    ds[x >> 1] = pack_bf16x2(a, b);
                 }
+                tmem_st16(tS, ds);
                 tmem_wait_st();
             }
             tc_fence_before();
             warp_arrive(&bar[C::ds_full + (i & 1)], lane);
         }
-        if (!joined) named_bar(1, NEL);  // left early: the other warps still come by
+        if (!joined) join();  // no step in the second pass, or left early: the other warps still come by
         if (!w.stopped()) {
-            w.wait(&bar[C::dq_done + ((steps - 1) & 1)], (steps - 1) >> 1);
+            w.wait(&bar[C::all_done], 0);
             tc_fence_after();
-            if (!w.stopped() && g == 0)
-                store_rows<D>(tmem + lanes + C::tQ, scale, sm + C::Q, wq, lane, dq + (row0 * Hq + h) * D, (int64_t)Hq * D,
-                              rows);
+            if (!w.stopped() && g < 2)
+                store_rows<D, D / 2>(tmem + lanes + C::tQ, scale, sm + C::Q, wq, lane, g * (D / 2),
+                                     dq + (row0 * Hq + h) * D, (int64_t)Hq * D, rows);
         }
     }
-    if (w.aborted() && warp == 9 && lane == 0) drain_loads(bar, C::q_full, 1 + NK + NV);
+    if (w.aborted() && warp == 19 && lane == 0) drain_loads(bar, C::q_full, 1 + NK + NV);
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 19) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -345,17 +357,18 @@ template <int D> struct DkvCfg {
     static constexpr int o_full = q_full + NS;     // [NS] dO
     static constexpr int empty = o_full + NS;      // [NS] the stage has been used
     static constexpr int zeroed = empty + NS;      // [NS] the stage has no row behind the end (ragged ends only)
-    static constexpr int s_full = zeroed + NS;
-    static constexpr int dp_full = s_full + 1;
-    static constexpr int p_half = dp_full + 1;     // [2] columns 0-63, 64-127 of P^T are there
-    static constexpr int ds_full = p_half + 2;
-    static constexpr int dv_done = ds_full + 1;    // P^T has been used
-    static constexpr int dk_done = dv_done + 1;    // dS^T has been used
-    static constexpr int drain = dk_done + 1;
-    static constexpr int NBAR = drain + 1;
+    static constexpr int s_full = zeroed + NS;     // [2]
+    static constexpr int dp_full = s_full + 2;     // [2]
+    static constexpr int p_full = dp_full + 2;     // [2] P^T is there
+    static constexpr int ds_full = p_full + 2;     // [2] dS^T is there
+    static constexpr int dv_done = ds_full + 2;    // [2] P^T has been used
+    static constexpr int dk_done = dv_done + 2;    // [2] dS^T has been used
+    static constexpr int all_done = dk_done + 2;   // dV and dK are there
+    static constexpr int drain = all_done + 1;     // [3]
+    static constexpr int NBAR = drain + 3;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
-    static constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // S^T, dP^T, dV, dK
+    static constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // S^T[2], dP^T[2], dV, dK
 };
 
 template <int D>
@@ -381,7 +394,8 @@ __global__ void __launch_bounds__(NTH, 1)
     const int hk = blockIdx.x % Hk, G = Hq / Hk;
     const int blocks = (at.len + BT - 1) / BT;
     const int kb = blocks - 1 - at.block;          // the first key blocks see the most queries
-    const int n = blocks - kb;                     // query blocks per head
+    const int n = (at.len - kb * BT + HT - 1) / HT;  // steps per head
+    const int nt = blocks - kb;                    // query tiles per head
     const int steps = G * n;
     const int rows = at.len - kb * BT;             // keys that exist
     const int tail = at.len - (blocks - 1) * BT;   // queries of the last block
@@ -391,13 +405,13 @@ __global__ void __launch_bounds__(NTH, 1)
         for (int i = 0; i < C::NBAR; ++i) {
             int c = 1;
             if (i >= C::q_full && i < C::o_full) c = 1 + 32;
-            if ((i >= C::p_half && i < C::ds_full) || i == C::ds_full) c = NEL / 32;  // one a warp
+            if (i >= C::p_full && i < C::dv_done) c = NEL / 64;  // one a warp
             mbar_init(&bar[i], c);
         }
         fence_mbar_init();
         *abort_flag = 0;
     }
-    if (warp == 9) {
+    if (warp == 19) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -406,173 +420,169 @@ __global__ void __launch_bounds__(NTH, 1)
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-    if (warp == 9) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&bar[C::kv_full], 2 * C::TILE);
-            load_tile<D>(sm + C::K, &tmK, &bar[C::kv_full], hk, (int)row0);
-            load_tile<D>(sm + C::V, &tmV, &bar[C::kv_full], hk, (int)row0);
-        }
-        for (int i = 0; i < steps; ++i) {
-            const int s = i % NS, h = hk * G + i / n, qb = kb + i % n;
-            if (i >= NS) w.wait(&bar[C::empty + s], i / NS - 1);
-            if (w.stopped()) break;
-            const int64_t q0 = at.t0 + qb * BT;
+    // registers: as on the query side
+    if (warp >= 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 19) {
             if (lane == 0) {
-                mbar_arrive_expect_tx(&bar[C::q_full + s], C::TILE);
-                load_tile<D>(sm + C::Q + s * C::TILE, &tmQ, &bar[C::q_full + s], h, (int)q0);
-                mbar_arrive_expect_tx(&bar[C::o_full + s], C::TILE);
-                load_tile<D>(sm + C::O + s * C::TILE, &tmO, &bar[C::o_full + s], h, (int)q0);
+                mbar_arrive_expect_tx(&bar[C::kv_full], 2 * C::TILE);
+                load_tile<D>(sm + C::K, &tmK, &bar[C::kv_full], hk, (int)row0);
+                load_tile<D>(sm + C::V, &tmV, &bar[C::kv_full], hk, (int)row0);
             }
-            // rows behind the end get 0, 0: a weight of 1 on a row of zeros
-            float *st = reinterpret_cast<float *>(sm + C::ST) + s * 2 * BT;
-            const int live = qb == blocks - 1 ? tail : BT;
-#pragma unroll
-            for (int x = lane; x < BT; x += 32) {
-                const int64_t o = (int64_t)h * tokens + q0 + min(x, live - 1);
-                cp_async_4(st + x, nlse + o, x < live ? 4u : 0u);
-                cp_async_4(st + BT + x, ndot + o, x < live ? 4u : 0u);
-            }
-            cp_async_mbar_arrive(&bar[C::q_full + s]);
-            if (qb == blocks - 1 && tail < BT) {
-                w.wait(&bar[C::q_full + s], i / NS);
-                w.wait(&bar[C::o_full + s], i / NS);
+            for (int i = 0; i < G * nt; ++i) {
+                const int s = i % NS, h = hk * G + i / nt, qb = kb + i % nt;
+                if (i >= NS) w.wait(&bar[C::empty + s], i / NS - 1);
                 if (w.stopped()) break;
-                zero_rows<D>(sm + C::Q + s * C::TILE, tail, lane);
-                zero_rows<D>(sm + C::O + s * C::TILE, tail, lane);
+                const int64_t q0 = at.t0 + qb * BT;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar[C::q_full + s], C::TILE);
+                    load_tile<D>(sm + C::Q + s * C::TILE, &tmQ, &bar[C::q_full + s], h, (int)q0);
+                    mbar_arrive_expect_tx(&bar[C::o_full + s], C::TILE);
+                    load_tile<D>(sm + C::O + s * C::TILE, &tmO, &bar[C::o_full + s], h, (int)q0);
+                }
+                // rows behind the end get 0, 0: a weight of 1 on a row of zeros
+                float *st = reinterpret_cast<float *>(sm + C::ST) + s * 2 * BT;
+                const int live = qb == blocks - 1 ? tail : BT;
+#pragma unroll
+                for (int x = lane; x < BT; x += 32) {
+                    const int64_t o = (int64_t)h * tokens + q0 + min(x, live - 1);
+                    cp_async_4(st + x, nlse + o, x < live ? 4u : 0u);
+                    cp_async_4(st + BT + x, ndot + o, x < live ? 4u : 0u);
+                }
+                cp_async_mbar_arrive(&bar[C::q_full + s]);
+                if (qb == blocks - 1 && tail < BT) {
+                    w.wait(&bar[C::q_full + s], i / NS);
+                    w.wait(&bar[C::o_full + s], i / NS);
+                    if (w.stopped()) break;
+                    zero_rows<D>(sm + C::Q + s * C::TILE, tail, lane);
+                    zero_rows<D>(sm + C::O + s * C::TILE, tail, lane);
+                }
+                if (tail < BT && lane == 0) arrive(&bar[C::zeroed + s]);
+                __syncwarp();
             }
-            if (tail < BT && lane == 0) arrive(&bar[C::zeroed + s]);
-            __syncwarp();
-        }
-    } else if (warp == 8) {
-        {
-            auto arrived = [&](int first, int i) {
-                w.wait(&bar[first + i % NS], i / NS);
-                if (tail < BT) w.wait(&bar[C::zeroed + i % NS], i / NS);
-            };
-            auto scores = [&](int i) {
-                arrived(C::q_full, i);
-                tc_fence_after();
-                mma_nt<D>(tmem + C::tS, sm + C::K, sm + C::Q + (i % NS) * C::TILE);
-                commit(&bar[C::s_full]);
-            };
-            auto dprobs = [&](int i) {
-                arrived(C::o_full, i);
-                tc_fence_after();
-                mma_nt<D>(tmem + C::tP, sm + C::V, sm + C::O + (i % NS) * C::TILE);
-                commit(&bar[C::dp_full]);
-            };
+        } else if (warp == 16) {  // S^T
             w.wait(&bar[C::kv_full], 0);
-            scores(0);
-            dprobs(0);
-            for (int i = 0; i < steps && !w.stopped(); ++i) {
-                const unsigned char *q = sm + C::Q + (i % NS) * C::TILE, *o = sm + C::O + (i % NS) * C::TILE;
-                w.wait(&bar[C::p_half], i);
-                tc_fence_after();
-                mma_chunks<D>(tmem + C::tV, tmem + C::tS, o, 0, 4, i > 0);
-                w.wait(&bar[C::p_half + 1], i);
-                tc_fence_after();
-                mma_chunks<D>(tmem + C::tV, tmem + C::tS, o, 4, 8, true);
-                commit(&bar[C::dv_done]);
-                if (i + 1 < steps) {  // over P^T; it runs while dS^T is formed
-                    w.wait(&bar[C::dv_done], i);
-                    scores(i + 1);
+            for (int g = 0, i = 0; g < G; ++g)
+                for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
+                    const int j = g * nt + (x >> 1), s = j % NS;
+                    if (i > 1) w.wait(&bar[C::dv_done + (i & 1)], (i >> 1) - 1);
+                    w.wait(&bar[C::q_full + s], j / NS);
+                    if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
+                    tc_fence_after();
+                    mma_nt<D, HT>(tmem + C::tS + HT * (i & 1), sm + C::K, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
+                    commit(&bar[C::s_full + (i & 1)]);
                 }
-                w.wait(&bar[C::ds_full], i);
-                tc_fence_after();
-                mma_chunks<D>(tmem + C::tK, tmem + C::tP, q, 0, 8, i > 0);
-                commit(&bar[C::dk_done]);
-                commit(&bar[C::empty + i % NS]);
-                if (i + 1 < steps) {  // over dS^T; it runs while the next P^T is formed
-                    w.wait(&bar[C::dk_done], i);
-                    dprobs(i + 1);
+        } else if (warp == 17) {  // dP^T
+            w.wait(&bar[C::kv_full], 0);
+            for (int g = 0, i = 0; g < G; ++g)
+                for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
+                    const int j = g * nt + (x >> 1), s = j % NS;
+                    if (i > 1) w.wait(&bar[C::dk_done + (i & 1)], (i >> 1) - 1);
+                    w.wait(&bar[C::o_full + s], j / NS);
+                    if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
+                    tc_fence_after();
+                    mma_nt<D, HT>(tmem + C::tP + HT * (i & 1), sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
+                    commit(&bar[C::dp_full + (i & 1)]);
                 }
-            }
-            if (w.stopped()) {
-                commit(&bar[C::drain]);
-                mbar_wait_bounded(&bar[C::drain], 0, 100000000ull);
-            }
+        } else {  // dV, dK
+            for (int g = 0, i = 0; g < G; ++g)
+                for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
+                    const int j = g * nt + (x >> 1), s = j % NS, at_ = s * C::TILE + (x & 1) * kHalf;
+                    w.wait(&bar[C::o_full + s], j / NS);
+                    if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
+                    w.wait(&bar[C::p_full + (i & 1)], i >> 1);
+                    tc_fence_after();
+                    mma_step<D>(tmem + C::tV, tmem + C::tS + HT * (i & 1), sm + C::O + at_, i > 0);
+                    commit(&bar[C::dv_done + (i & 1)]);
+                    w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
+                    tc_fence_after();
+                    mma_step<D>(tmem + C::tK, tmem + C::tP + HT * (i & 1), sm + C::Q + at_, i > 0);
+                    commit(&bar[C::dk_done + (i & 1)]);
+                    if ((x & 1) || x == n - 1) commit(&bar[C::empty + s]);
+                }
+            commit(&bar[C::all_done]);
+        }
+        if (warp < 19 && w.stopped()) {  // products issued already end before the tensor memory is freed
+            commit(&bar[C::drain + warp - 16]);
+            mbar_wait_bounded(&bar[C::drain + warp - 16], 0, 100000000ull);
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int g = warp >> 2, wq = warp & 3, r = tid & (BT - 1);  // r: key row
+        const int set = g >> 1, c0 = 32 * (g & 1);  // steps of this parity, these columns
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
-        const uint32_t tS = tmem + lanes + C::tS, tP = tmem + lanes + C::tP;
+        const uint32_t tS = tmem + lanes + C::tS + HT * set + c0, tP = tmem + lanes + C::tP + HT * set + c0;
         const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e);
-        for (int i = 0; i < steps; ++i) {
-            const int s = i % NS;
-            const float *st = reinterpret_cast<const float *>(sm + C::ST) + s * 2 * BT;
-            float p[2][32];
-            w.wait(&bar[C::q_full + s], i / NS);
-            w.wait(&bar[C::s_full], i);
+        for (int i = set; i < steps; i += 2) {
+            const int x0 = i % n, j = i / n * nt + (x0 >> 1), s = j % NS;
+            const float *st = reinterpret_cast<const float *>(sm + C::ST) + s * 2 * BT + (x0 & 1) * HT + c0;
+            float p[32];
+            w.wait(&bar[C::s_full + (i & 1)], i >> 1);
+            w.wait(&bar[C::q_full + s], j / NS);  // over by now: for the rows' -lse and -D
             if (w.stopped()) break;
             tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) tmem_ld32(tS + 64 * q + 32 * g, p[q]);
+            tmem_ld32(tS, p);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int c0 = 64 * q + 32 * g;
+            for (int x = 0; x < 32; x += 4) {
+                const float4 nl = *reinterpret_cast<const float4 *>(st + x);
+                unpack2(fma2(pack2(p[x], p[x + 1]), sc2, pack2(nl.x, nl.y)), p[x], p[x + 1]);
+                unpack2(fma2(pack2(p[x + 2], p[x + 3]), sc2, pack2(nl.z, nl.w)), p[x + 2], p[x + 3]);
 #pragma unroll
-                for (int x = 0; x < 32; x += 4) {
-                    const float4 nl = *reinterpret_cast<const float4 *>(st + c0 + x);
-                    unpack2(fma2(pack2(p[q][x], p[q][x + 1]), sc2, pack2(nl.x, nl.y)), p[q][x], p[q][x + 1]);
-                    unpack2(fma2(pack2(p[q][x + 2], p[q][x + 3]), sc2, pack2(nl.z, nl.w)), p[q][x + 2], p[q][x + 3]);
+                for (int e = 0; e < 4; ++e) p[x + e] = ex2_approx(p[x + e]);
+            }
+            if (x0 < 2) {  // the diagonal block: queries before the key
+                const int q0 = x0 * HT + c0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[q][x + e] = ex2_approx(p[q][x + e]);
-                }
-                if (i % n == 0) {  // the diagonal block: queries before the key
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (c0 + x < r) p[q][x] = 0.f;
-                }
+                for (int x = 0; x < 32; ++x)
+                    if (q0 + x < r) p[x] = 0.f;
+            }
+            {
                 uint32_t pk[16];
 #pragma unroll
-                for (int x = 0; x < 32; x += 2) pk[x >> 1] = pack_bf16x2(p[q][x], p[q][x + 1]);
-                tmem_st16(tS + c0, pk);
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(&bar[C::p_half + q], lane);
-            }
-            w.wait(&bar[C::dp_full], i);
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int c0 = 64 * q + 32 * g;
-                float dp[32];
-                tmem_ld32(tP + c0, dp);
-                tmem_wait_ld();
-                uint32_t ds[16];
-#pragma unroll
-                for (int x = 0; x < 32; x += 4) {
-                    const float4 nd = *reinterpret_cast<const float4 *>(st + BT + c0 + x);
-                    float a, b;
-                    unpack2(mul2(pack2(p[q][x], p[q][x + 1]), add2(pack2(dp[x], dp[x + 1]), pack2(nd.x, nd.y))), a, b);
-                    ds[x >> 1] = pack_bf16x2(a, b);
-                    unpack2(mul2(pack2(p[q][x + 2], p[q][x + 3]), add2(pack2(dp[x + 2], dp[x + 3]), pack2(nd.z, nd.w))), a, b);
-                    ds[(x >> 1) + 1] = pack_bf16x2(a, b);
-                }
-                tmem_st16(tP + c0, ds);
+                for (int x = 0; x < 16; ++x) pk[x] = pack_bf16x2(p[2 * x], p[2 * x + 1]);
+                tmem_st16(tS, pk);
             }
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&bar[C::ds_full], lane);
+            warp_arrive(&bar[C::p_full + (i & 1)], lane);
+            w.wait(&bar[C::dp_full + (i & 1)], i >> 1);
+            tc_fence_after();
+            float dp[32];
+            tmem_ld32(tP, dp);
+            tmem_wait_ld();
+            uint32_t ds[16];
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+                const float4 nd = *reinterpret_cast<const float4 *>(st + BT + x);
+                float a, b;
+                unpack2(mul2(pack2(p[x], p[x + 1]), add2(pack2(dp[x], dp[x + 1]), pack2(nd.x, nd.y))), a, b);
+                ds[x >> 1] = pack_bf16x2(a, b);
+                unpack2(mul2(pack2(p[x + 2], p[x + 3]), add2(pack2(dp[x + 2], dp[x + 3]), pack2(nd.z, nd.w))), a, b);
+                ds[(x >> 1) + 1] = pack_bf16x2(a, b);
+            }
+            tmem_st16(tP, ds);
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bar[C::ds_full + (i & 1)], lane);
         }
         if (!w.stopped()) {
-            w.wait(&bar[C::dk_done], steps - 1);
+            w.wait(&bar[C::all_done], 0);
             tc_fence_after();
-            if (!w.stopped()) {  // group 0 stores dV, group 1 dK
-                __nv_bfloat16 *to = (g ? dk : dv) + (row0 * Hk + hk) * D;
-                store_rows<D>(tmem + lanes + (g ? C::tK : C::tV), g ? scale : 1.f, sm + (g ? C::K : C::V), wq, lane, to,
-                              (int64_t)Hk * D, rows);
+            if (!w.stopped()) {  // groups 0 and 1 store dV, 2 and 3 dK
+                __nv_bfloat16 *to = (g >= 2 ? dk : dv) + (row0 * Hk + hk) * D;
+                store_rows<D, D / 2>(tmem + lanes + (g >= 2 ? C::tK : C::tV), g >= 2 ? scale : 1.f,
+                                     sm + (g >= 2 ? C::K : C::V), wq, lane, (g & 1) * (D / 2), to, (int64_t)Hk * D, rows);
             }
         }
     }
-    if (w.aborted() && warp == 9) {
+    if (w.aborted() && warp == 19) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (lane == 0) drain_loads(bar, C::kv_full, 1 + 2 * NS);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 19) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
