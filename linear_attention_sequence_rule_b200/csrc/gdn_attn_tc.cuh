@@ -169,6 +169,43 @@ template <int D, int N = BT> __device__ __forceinline__ void mma_nt(uint32_t d, 
     }
 }
 
+// The same with A (128 rows of D, bf16: D / 2 columns) in tensor memory
+template <int D, int N = BT> __device__ __forceinline__ void mma_nt_ta(uint32_t d, uint32_t a, const unsigned char *b)
+{
+    constexpr uint32_t id = idesc_bf16(BT, N, 0, 0);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+        mma_ts(d, a + 8 * kk, sdesc_sw128(smem_u32(b) + (kk >> 2) * kSub + (kk & 3) * 32, 16, 1024), id, kk > 0);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Elements e0 .. e0 + NE - 1 of row r of a tile in shared memory to tensor memory (address t of the row's
+// element 0, the warp's lanes included).  Operands that stay for a whole CTA are kept there: a product
+// of two shared operands takes all of shared memory's bandwidth, and every other access (a barrier's
+// probe, a row's statistics) then waits some 300 cycles.
+template <int NE> __device__ __forceinline__ void row_to_tmem(uint32_t t, const unsigned char *tile, int r, int e0)
+{
+#pragma unroll
+    for (int x = 0; x < NE / 32; ++x) {
+        uint32_t v[16];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int c = e0 / 8 + 4 * x + u;  // 16-byte unit of the row
+            const uint4 y = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * kSub + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            v[4 * u] = y.x, v[4 * u + 1] = y.y, v[4 * u + 2] = y.z, v[4 * u + 3] = y.w;
+        }
+        tmem_st16(t + (e0 + 32 * x) / 2, v);
+    }
+}
+
 // D[128 x D] (+)= A B: A (128 x 128, bf16) in tensor memory, B's rows (the 128 of the sum) in shared
 // memory, read MN-major; k steps k0 .. k1 - 1 of 16
 template <int D>

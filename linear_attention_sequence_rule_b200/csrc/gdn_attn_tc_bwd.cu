@@ -21,7 +21,9 @@
 // that the products of one step run while the other's elements are worked on.  Steps of 128 with one
 // dP (or, on the key side, one S) buffer spend half their time in the chain of waits between products
 // and elements (about 1900 cycles a step with products and exponentials taken out); a product 64 wide
-// takes 48 cycles for 32 cycles' work (both operands come from shared memory), and is still faster.
+// of two shared operands takes 48 cycles for 32 cycles' work, so the operands that stay for the whole CTA
+// are moved to tensor memory: Q and dO on the query side, K and (at d = 64) V on the key side.  At d = 128
+// the key side has no room for V and for a second dP beside K.
 //   warps 0-7, 8-15  element by element, the even and the odd steps: a thread has a row, 32 columns
 //   warps 16-18      issue the products
 //   warp 19          loads; zeroes rows behind the sequence's end
@@ -59,15 +61,6 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, const unsigned 
                accumulate || kk > 0);
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&v)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
 __device__ __forceinline__ void named_bar(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 // After a wait ran out: copies in flight end before the CTA does.
@@ -99,13 +92,15 @@ template <int D> struct DqCfg {
     static constexpr int dp_free = dp_full + 2;    // [2] dP has been read
     static constexpr int ds_full = dp_free + 2;    // [2] dS is there (first pass: S has been read)
     static constexpr int dq_done = ds_full + 2;    // [2] dS has been used
-    static constexpr int all_done = dq_done + 2;   // dQ is there (a barrier of one phase: a warp that
+    static constexpr int a_full = dq_done + 2;     // Q and dO are in tensor memory
+    static constexpr int all_done = a_full + 1;    // dQ is there (a barrier of one phase: a warp that
                                                    // passes over phases cannot tell them by parity)
     static constexpr int drain = all_done + 1;     // [3]
     static constexpr int NBAR = drain + 3;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
-    static constexpr uint32_t tS = 0, tP = 128, tQ = 256;  // S[2], dP[2], dQ
+    static constexpr uint32_t tS = 0, tP = 128, tG = 256, tQ = 256 + D, tO = tQ + D / 2;  // S[2], dP[2], dQ, Q, dO
+    static_assert(tO + D / 2 <= 512, "tensor memory budget");
     static_assert(TOTAL <= 232448, "shared memory budget");
 };
 
@@ -140,7 +135,7 @@ __global__ void __launch_bounds__(NTH, 1)
 
     if (tid == 0) {
         for (int i = 0; i < C::NBAR; ++i)
-            mbar_init(&bar[i], i >= C::dp_free && i < C::dq_done ? NEL / 64 : 1);  // one a warp
+            mbar_init(&bar[i], i == C::a_full ? NEL / 32 : i >= C::dp_free && i < C::dq_done ? NEL / 64 : 1);  // one a warp
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -193,7 +188,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 }
             }
         } else if (warp == 16) {  // S
-            w.wait(&bar[C::q_full], 0);
+            w.wait(&bar[C::a_full], 0);
             for (int p = 0, i = 0; p < passes; ++p)
                 for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
                     const int j = p * nt + (s >> 1);
@@ -201,11 +196,11 @@ __global__ void __launch_bounds__(NTH, 1)
                     w.wait(&bar[C::k_full + j % NK], j / NK);
                     if (rows < BT) w.wait(&bar[C::k_zeroed + j % NK], j / NK);
                     tc_fence_after();
-                    mma_nt<D, HT>(tmem + C::tS + HT * (i & 1), sm + C::Q, sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf);
+                    mma_nt_ta<D, HT>(tmem + C::tS + HT * (i & 1), tmem + C::tQ, sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf);
                     commit(&bar[C::s_full + (i & 1)]);
                 }
         } else if (warp == 17) {  // dP
-            w.wait(&bar[C::q_full], 0);
+            w.wait(&bar[C::a_full], 0);
             for (int p = 0, i = 0; p < passes; ++p)
                 for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
                     const int j = p * nt + (s >> 1);
@@ -213,7 +208,7 @@ __global__ void __launch_bounds__(NTH, 1)
                     w.wait(&bar[C::v_full + j % NV], j / NV);
                     if (rows < BT) w.wait(&bar[C::v_zeroed + j % NV], j / NV);
                     tc_fence_after();
-                    mma_nt<D, HT>(tmem + C::tP + HT * (i & 1), sm + C::O, sm + C::V + (j % NV) * C::TILE + (s & 1) * kHalf);
+                    mma_nt_ta<D, HT>(tmem + C::tP + HT * (i & 1), tmem + C::tO, sm + C::V + (j % NV) * C::TILE + (s & 1) * kHalf);
                     commit(&bar[C::dp_full + (i & 1)]);
                     if ((s & 1) || s == n - 1) commit(&bar[C::v_empty + j % NV]);
                 }
@@ -224,7 +219,7 @@ __global__ void __launch_bounds__(NTH, 1)
                     w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
                     tc_fence_after();
                     if (p == passes - 1)
-                        mma_step<D>(tmem + C::tQ, tmem + C::tS + HT * (i & 1),
+                        mma_step<D>(tmem + C::tG, tmem + C::tS + HT * (i & 1),
                                     sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf, s > 0);
                     commit(&bar[C::dq_done + (i & 1)]);
                     if ((s & 1) || s == n - 1) commit(&bar[C::k_empty + j % NK]);
@@ -243,8 +238,12 @@ __global__ void __launch_bounds__(NTH, 1)
         const bool live = r < rows;
         const float nl = live ? -lse[(row0 + r) * Hq + h] * kLog2e : 0.f;
         float nd = 0.f;
+        w.wait(&bar[C::q_full], 0);  // groups 0, 1: halves of Q's rows, 2, 3: of dO's
+        row_to_tmem<D / 2>(tmem + lanes + (g < 2 ? C::tQ : C::tO), sm + (g < 2 ? C::Q : C::O), r, (g & 1) * (D / 2));
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&bar[C::a_full], lane);
         if (!exact) {  // D from out: this thread's quarter of the row
-            w.wait(&bar[C::q_full], 0);
             if (live) {
                 const uint4 *o = reinterpret_cast<const uint4 *>(out + ((row0 + r) * Hq + h) * D) + g * (D / 32);
 #pragma unroll
@@ -333,7 +332,7 @@ __global__ void __launch_bounds__(NTH, 1)
             w.wait(&bar[C::all_done], 0);
             tc_fence_after();
             if (!w.stopped() && g < 2)
-                store_rows<D, D / 2>(tmem + lanes + C::tQ, scale, sm + C::Q, wq, lane, g * (D / 2),
+                store_rows<D, D / 2>(tmem + lanes + C::tG, scale, sm + C::Q, wq, lane, g * (D / 2),
                                      dq + (row0 * Hq + h) * D, (int64_t)Hq * D, rows);
         }
     }
@@ -363,12 +362,16 @@ template <int D> struct DkvCfg {
     static constexpr int ds_full = p_full + 2;     // [2] dS^T is there
     static constexpr int dv_done = ds_full + 2;    // [2] P^T has been used
     static constexpr int dk_done = dv_done + 2;    // [2] dS^T has been used
-    static constexpr int all_done = dk_done + 2;   // dV and dK are there
+    static constexpr int a_full = dk_done + 2;     // K (and V) are in tensor memory
+    static constexpr int all_done = a_full + 1;    // dV and dK are there
     static constexpr int drain = all_done + 1;     // [3]
     static constexpr int NBAR = drain + 3;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
-    static constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // S^T[2], dP^T[2], dV, dK
+    static constexpr bool TV = D == 64;            // V in tensor memory, two dP tiles
+    // S^T[2], dP^T[1 or 2], dV, dK, K, V
+    static constexpr uint32_t tS = 0, tP = 128, tGV = tP + HT * (TV ? 2 : 1), tGK = tGV + D, tK = tGK + D, tV = tK + D / 2;
+    static_assert(tV + (TV ? D / 2 : 0) <= 512, "tensor memory budget");
 };
 
 template <int D>
@@ -406,6 +409,7 @@ __global__ void __launch_bounds__(NTH, 1)
             int c = 1;
             if (i >= C::q_full && i < C::o_full) c = 1 + 32;
             if (i >= C::p_full && i < C::dv_done) c = NEL / 64;  // one a warp
+            if (i == C::a_full) c = NEL / 32;
             mbar_init(&bar[i], c);
         }
         fence_mbar_init();
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 __syncwarp();
             }
         } else if (warp == 16) {  // S^T
-            w.wait(&bar[C::kv_full], 0);
+            w.wait(&bar[C::a_full], 0);
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
@@ -469,19 +473,27 @@ __global__ void __launch_bounds__(NTH, 1)
                     w.wait(&bar[C::q_full + s], j / NS);
                     if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     tc_fence_after();
-                    mma_nt<D, HT>(tmem + C::tS + HT * (i & 1), sm + C::K, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
+                    mma_nt_ta<D, HT>(tmem + C::tS + HT * (i & 1), tmem + C::tK, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
                     commit(&bar[C::s_full + (i & 1)]);
                 }
         } else if (warp == 17) {  // dP^T
             w.wait(&bar[C::kv_full], 0);
+            w.wait(&bar[C::a_full], 0);
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
-                    if (i > 1) w.wait(&bar[C::dk_done + (i & 1)], (i >> 1) - 1);
+                    if (C::TV) {
+                        if (i > 1) w.wait(&bar[C::dk_done + (i & 1)], (i >> 1) - 1);
+                    } else {
+                        if (i > 0) w.wait(&bar[C::dk_done + ((i - 1) & 1)], (i - 1) >> 1);
+                    }
                     w.wait(&bar[C::o_full + s], j / NS);
                     if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     tc_fence_after();
-                    mma_nt<D, HT>(tmem + C::tP + HT * (i & 1), sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
+                    if (C::TV)
+                        mma_nt_ta<D, HT>(tmem + C::tP + HT * (i & 1), tmem + C::tV, sm + C::O + s * C::TILE + (x & 1) * kHalf);
+                    else
+                        mma_nt<D, HT>(tmem + C::tP, sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
                     commit(&bar[C::dp_full + (i & 1)]);
                 }
         } else {  // dV, dK
@@ -492,11 +504,11 @@ __global__ void __launch_bounds__(NTH, 1)
                     if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     w.wait(&bar[C::p_full + (i & 1)], i >> 1);
                     tc_fence_after();
-                    mma_step<D>(tmem + C::tV, tmem + C::tS + HT * (i & 1), sm + C::O + at_, i > 0);
+                    mma_step<D>(tmem + C::tGV, tmem + C::tS + HT * (i & 1), sm + C::O + at_, i > 0);
                     commit(&bar[C::dv_done + (i & 1)]);
                     w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
                     tc_fence_after();
-                    mma_step<D>(tmem + C::tK, tmem + C::tP + HT * (i & 1), sm + C::Q + at_, i > 0);
+                    mma_step<D>(tmem + C::tGK, tmem + C::tP + (C::TV ? HT * (i & 1) : 0), sm + C::Q + at_, i > 0);
                     commit(&bar[C::dk_done + (i & 1)]);
                     if ((x & 1) || x == n - 1) commit(&bar[C::empty + s]);
                 }
@@ -511,8 +523,14 @@ __global__ void __launch_bounds__(NTH, 1)
         const int g = warp >> 2, wq = warp & 3, r = tid & (BT - 1);  // r: key row
         const int set = g >> 1, c0 = 32 * (g & 1);  // steps of this parity, these columns
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
-        const uint32_t tS = tmem + lanes + C::tS + HT * set + c0, tP = tmem + lanes + C::tP + HT * set + c0;
+        const uint32_t tS = tmem + lanes + C::tS + HT * set + c0, tP = tmem + lanes + C::tP + (C::TV ? HT * set : 0) + c0;
         const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e);
+        w.wait(&bar[C::kv_full], 0);
+        if (C::TV || g < 2)  // groups 0, 1: halves of K's rows, 2, 3: of V's
+            row_to_tmem<D / 2>(tmem + lanes + (g < 2 ? C::tK : C::tV), sm + (g < 2 ? C::K : C::V), r, (g & 1) * (D / 2));
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&bar[C::a_full], lane);
         for (int i = set; i < steps; i += 2) {
             const int x0 = i % n, j = i / n * nt + (x0 >> 1), s = j % NS;
             const float *st = reinterpret_cast<const float *>(sm + C::ST) + s * 2 * BT + (x0 & 1) * HT + c0;
@@ -571,7 +589,7 @@ __global__ void __launch_bounds__(NTH, 1)
             tc_fence_after();
             if (!w.stopped()) {  // groups 0 and 1 store dV, 2 and 3 dK
                 __nv_bfloat16 *to = (g >= 2 ? dk : dv) + (row0 * Hk + hk) * D;
-                store_rows<D, D / 2>(tmem + lanes + (g >= 2 ? C::tK : C::tV), g >= 2 ? scale : 1.f,
+                store_rows<D, D / 2>(tmem + lanes + (g >= 2 ? C::tGK : C::tGV), g >= 2 ? scale : 1.f,
                                      sm + (g >= 2 ? C::K : C::V), wq, lane, (g & 1) * (D / 2), to, (int64_t)Hk * D, rows);
             }
         }
