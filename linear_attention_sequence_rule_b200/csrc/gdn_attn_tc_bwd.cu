@@ -22,8 +22,8 @@
 // dP (or, on the key side, one S) buffer spend half their time in the chain of waits between products
 // and elements (about 1900 cycles a step with products and exponentials taken out); a product 64 wide
 // of two shared operands takes 48 cycles for 32 cycles' work, so the operands that stay for the whole CTA
-// are moved to tensor memory: Q and dO on the query side, K and (at d = 64) V on the key side.  At d = 128
-// the key side has no room for V and for a second dP beside K.
+// are moved to tensor memory: Q and dO on the query side, K and V on the key side at d = 64 (at d = 128 there
+// is no room for them; with K there and one dP tile a step takes 1920 cycles, with two dP tiles 1640).
 //   warps 0-7, 8-15  element by element, the even and the odd steps: a thread has a row, 32 columns
 //   warps 16-18      issue the products
 //   warp 19          loads; zeroes rows behind the sequence's end
@@ -89,8 +89,8 @@ template <int D> struct DqCfg {
     static constexpr int v_zeroed = k_zeroed + NK; // [NV]
     static constexpr int s_full = v_zeroed + NV;   // [2]
     static constexpr int dp_full = s_full + 2;     // [2]
-    static constexpr int dp_free = dp_full + 2;    // [2] dP has been read
-    static constexpr int ds_full = dp_free + 2;    // [2] dS is there (first pass: S has been read)
+    static constexpr int s_free = dp_full + 2;     // [2] S has been read
+    static constexpr int ds_full = s_free + 2;     // [2] dS is there (first pass: dP has been read)
     static constexpr int dq_done = ds_full + 2;    // [2] dS has been used
     static constexpr int a_full = dq_done + 2;     // Q and dO are in tensor memory
     static constexpr int all_done = a_full + 1;    // dQ is there (a barrier of one phase: a warp that
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(NTH, 1)
 
     if (tid == 0) {
         for (int i = 0; i < C::NBAR; ++i)
-            mbar_init(&bar[i], i == C::a_full ? NEL / 32 : i >= C::dp_free && i < C::dq_done ? NEL / 64 : 1);  // one a warp
+            mbar_init(&bar[i], i == C::a_full ? NEL / 32 : i >= C::s_free && i < C::dq_done ? NEL / 64 : 1);  // one a warp
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -192,9 +192,9 @@ __global__ void __launch_bounds__(NTH, 1)
             for (int p = 0, i = 0; p < passes; ++p)
                 for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
                     const int j = p * nt + (s >> 1);
-                    if (i > 1) w.wait(&bar[C::dq_done + (i & 1)], (i >> 1) - 1);
                     w.wait(&bar[C::k_full + j % NK], j / NK);
                     if (rows < BT) w.wait(&bar[C::k_zeroed + j % NK], j / NK);
+                    if (i > 1) w.wait(&bar[C::s_free + (i & 1)], (i >> 1) - 1);
                     tc_fence_after();
                     mma_nt_ta<D, HT>(tmem + C::tS + HT * (i & 1), tmem + C::tQ, sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf);
                     commit(&bar[C::s_full + (i & 1)]);
@@ -204,9 +204,9 @@ __global__ void __launch_bounds__(NTH, 1)
             for (int p = 0, i = 0; p < passes; ++p)
                 for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
                     const int j = p * nt + (s >> 1);
-                    if (i > 1) w.wait(&bar[C::dp_free + (i & 1)], (i >> 1) - 1);
                     w.wait(&bar[C::v_full + j % NV], j / NV);
                     if (rows < BT) w.wait(&bar[C::v_zeroed + j % NV], j / NV);
+                    if (i > 1) w.wait(&bar[C::dq_done + (i & 1)], (i >> 1) - 1);
                     tc_fence_after();
                     mma_nt_ta<D, HT>(tmem + C::tP + HT * (i & 1), tmem + C::tO, sm + C::V + (j % NV) * C::TILE + (s & 1) * kHalf);
                     commit(&bar[C::dp_full + (i & 1)]);
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(NTH, 1)
                     w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
                     tc_fence_after();
                     if (p == passes - 1)
-                        mma_step<D>(tmem + C::tG, tmem + C::tS + HT * (i & 1),
+                        mma_step<D>(tmem + C::tG, tmem + C::tP + HT * (i & 1),
                                     sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf, s > 0);
                     commit(&bar[C::dq_done + (i & 1)]);
                     if ((s & 1) || s == n - 1) commit(&bar[C::k_empty + j % NK]);
@@ -288,6 +288,8 @@ __global__ void __launch_bounds__(NTH, 1)
             tc_fence_after();
             tmem_ld32(tS, s);
             tmem_wait_ld();
+            tc_fence_before();
+            warp_arrive(&bar[C::s_free + (i & 1)], lane);
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
                 unpack2(fma2(pack2(s[x], s[x + 1]), sc2, nl2), s[x], s[x + 1]);
@@ -304,8 +306,6 @@ __global__ void __launch_bounds__(NTH, 1)
             tc_fence_after();
             tmem_ld32(tP, dp);
             tmem_wait_ld();
-            tc_fence_before();
-            warp_arrive(&bar[C::dp_free + (i & 1)], lane);
             if (exact && i < n) {
                 uint64_t acc = 0;
 #pragma unroll
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(NTH, 1)
                     unpack2(mul2(pack2(s[x], s[x + 1]), add2(pack2(dp[x], dp[x + 1]), nd2)), a, b);
                     ds[x >> 1] = pack_bf16x2(a, b);
                 }
-                tmem_st16(tS, ds);
+                tmem_st16(tP, ds);
                 tmem_wait_st();
             }
             tc_fence_before();
@@ -368,10 +368,10 @@ template <int D> struct DkvCfg {
     static constexpr int NBAR = drain + 3;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
-    static constexpr bool TV = D == 64;            // V in tensor memory, two dP tiles
-    // S^T[2], dP^T[1 or 2], dV, dK, K, V
-    static constexpr uint32_t tS = 0, tP = 128, tGV = tP + HT * (TV ? 2 : 1), tGK = tGV + D, tK = tGK + D, tV = tK + D / 2;
-    static_assert(tV + (TV ? D / 2 : 0) <= 512, "tensor memory budget");
+    static constexpr bool TA = D == 64;            // K and V in tensor memory
+    // S^T[2], dP^T[2], dV, dK, (K, V)
+    static constexpr uint32_t tS = 0, tP = 128, tGV = 256, tGK = tGV + D, tK = tGK + D, tV = tK + D / 2;
+    static_assert(TA ? tV + D / 2 <= 512 : tK <= 512, "tensor memory budget");
 };
 
 template <int D>
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 __syncwarp();
             }
         } else if (warp == 16) {  // S^T
-            w.wait(&bar[C::a_full], 0);
+            w.wait(&bar[C::TA ? C::a_full : C::kv_full], 0);
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
@@ -473,27 +473,25 @@ __global__ void __launch_bounds__(NTH, 1)
                     w.wait(&bar[C::q_full + s], j / NS);
                     if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     tc_fence_after();
-                    mma_nt_ta<D, HT>(tmem + C::tS + HT * (i & 1), tmem + C::tK, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
+                    if (C::TA)
+                        mma_nt_ta<D, HT>(tmem + C::tS + HT * (i & 1), tmem + C::tK, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
+                    else
+                        mma_nt<D, HT>(tmem + C::tS + HT * (i & 1), sm + C::K, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
                     commit(&bar[C::s_full + (i & 1)]);
                 }
         } else if (warp == 17) {  // dP^T
-            w.wait(&bar[C::kv_full], 0);
-            w.wait(&bar[C::a_full], 0);
+            w.wait(&bar[C::TA ? C::a_full : C::kv_full], 0);
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
-                    if (C::TV) {
-                        if (i > 1) w.wait(&bar[C::dk_done + (i & 1)], (i >> 1) - 1);
-                    } else {
-                        if (i > 0) w.wait(&bar[C::dk_done + ((i - 1) & 1)], (i - 1) >> 1);
-                    }
+                    if (i > 1) w.wait(&bar[C::dk_done + (i & 1)], (i >> 1) - 1);
                     w.wait(&bar[C::o_full + s], j / NS);
                     if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     tc_fence_after();
-                    if (C::TV)
+                    if (C::TA)
                         mma_nt_ta<D, HT>(tmem + C::tP + HT * (i & 1), tmem + C::tV, sm + C::O + s * C::TILE + (x & 1) * kHalf);
                     else
-                        mma_nt<D, HT>(tmem + C::tP, sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
+                        mma_nt<D, HT>(tmem + C::tP + HT * (i & 1), sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
                     commit(&bar[C::dp_full + (i & 1)]);
                 }
         } else {  // dV, dK
@@ -508,7 +506,7 @@ __global__ void __launch_bounds__(NTH, 1)
                     commit(&bar[C::dv_done + (i & 1)]);
                     w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
                     tc_fence_after();
-                    mma_step<D>(tmem + C::tGK, tmem + C::tP + (C::TV ? HT * (i & 1) : 0), sm + C::Q + at_, i > 0);
+                    mma_step<D>(tmem + C::tGK, tmem + C::tP + HT * (i & 1), sm + C::Q + at_, i > 0);
                     commit(&bar[C::dk_done + (i & 1)]);
                     if ((x & 1) || x == n - 1) commit(&bar[C::empty + s]);
                 }
@@ -523,14 +521,15 @@ __global__ void __launch_bounds__(NTH, 1)
         const int g = warp >> 2, wq = warp & 3, r = tid & (BT - 1);  // r: key row
         const int set = g >> 1, c0 = 32 * (g & 1);  // steps of this parity, these columns
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
-        const uint32_t tS = tmem + lanes + C::tS + HT * set + c0, tP = tmem + lanes + C::tP + (C::TV ? HT * set : 0) + c0;
+        const uint32_t tS = tmem + lanes + C::tS + HT * set + c0, tP = tmem + lanes + C::tP + HT * set + c0;
         const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e);
-        w.wait(&bar[C::kv_full], 0);
-        if (C::TV || g < 2)  // groups 0, 1: halves of K's rows, 2, 3: of V's
+        if (C::TA) {  // groups 0, 1: halves of K's rows, 2, 3: of V's
+            w.wait(&bar[C::kv_full], 0);
             row_to_tmem<D / 2>(tmem + lanes + (g < 2 ? C::tK : C::tV), sm + (g < 2 ? C::K : C::V), r, (g & 1) * (D / 2));
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(&bar[C::a_full], lane);
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bar[C::a_full], lane);
+        }
         for (int i = set; i < steps; i += 2) {
             const int x0 = i % n, j = i / n * nt + (x0 >> 1), s = j % NS;
             const float *st = reinterpret_cast<const float *>(sm + C::ST) + s * 2 * BT + (x0 & 1) * HT + c0;
