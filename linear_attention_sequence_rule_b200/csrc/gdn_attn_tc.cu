@@ -5,14 +5,16 @@
 // lse = (m + log2 l) ln 2.
 //
 // One CTA holds two query tiles of 128 rows, which share every K and V tile that TMA brings (half the
-// L2 traffic of one tile).  Per tile, S (128 columns), O (D columns) and P (bf16, 64 columns; at
-// D = 128 over S's first columns, since S0, S1, O0, O1 fill the 512) sit in tensor memory.
+// L2 traffic of one tile).  They work in steps of 64 keys: a tile's O (D columns) and two (d = 128) or
+// three (d = 64) S tiles of 64 columns fill the 512 columns of tensor memory, and P (bf16) is written
+// over the S it came from.  So the scores of the next steps are formed while a step's softmax runs; with
+// one S tile of 128 keys a query tile had only one of the two under way, and a step of 128 keys took
+// 4500 cycles for 2048 of products or exponentials.
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread holds a row
 //   warps 8, 9       issue the MMAs of tile 0, 1
 //   warp 10          loads; zeroes V rows behind the sequence's end
-// The tiles run apart: while one's softmax runs on the CUDA cores, the other's products fill the tensor
-// pipe.  The maximum is moved only when a row's new one passes it by 2^8 (weights up to 2^8 are as
-// exact in bf16), so that O is rarely rescaled.
+// The maximum is moved only when a row's new one passes it by 2^8 (weights up to 2^8 are as exact in
+// bf16), so that O is rarely rescaled.
 #include <math.h>
 
 #include "gdn_attn_tc.cuh"
@@ -29,8 +31,11 @@ using namespace attn;
 
 constexpr int NTH = 384;
 
+constexpr int HT = 64;           // keys a step
+constexpr int kHalf = HT * 128;  // bytes from a tile's first half to its second (in each sub-tile)
+
 template <int D> struct FwdCfg {
-    static constexpr bool SEP = D == 64;      // P apart from S: the next S may come while P is formed
+    static constexpr int NB = D == 64 ? 3 : 2;  // S tiles
     static constexpr int NS = D == 64 ? 4 : 2;  // K and V stages
     static constexpr int TILE = BT * D * 2;
     static constexpr int Q = 0, K = 2 * TILE, V = K + NS * TILE, BAR = V + NS * TILE;
@@ -41,17 +46,18 @@ template <int D> struct FwdCfg {
     static constexpr int v_full = k_empty + NS;     // [NS]
     static constexpr int v_empty = v_full + NS;     // [NS]
     static constexpr int v_zeroed = v_empty + NS;   // [1]
-    static constexpr int s_full = v_zeroed + 1;     // [2] S of the block is there
-    static constexpr int s_free = s_full + 2;       // [2] S has been read (SEP)
-    static constexpr int p_half = s_free + 2;       // [2][2] columns 0-63, 64-127 of P are there
-    static constexpr int pv_done = p_half + 4;      // [2] O holds the block
-    static constexpr int drain = pv_done + 2;       // [2]
+    static constexpr int s_full = v_zeroed + 1;     // [2][NB] S of a step is there
+    static constexpr int p_full = s_full + 2 * NB;  // [2][NB] P of a step is there (one barrier a tile would not
+                                                    // do: a warp may be a step ahead of another)
+    static constexpr int pv_done = p_full + 2 * NB; // [2][2] by the step's parity: O holds the step
+    static constexpr int all_done = pv_done + 4;    // [2]
+    static constexpr int drain = all_done + 2;      // [2]
     static constexpr int NBAR = drain + 2;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
-    __host__ __device__ static constexpr uint32_t tS(int t) { return 128u * t; }
-    __host__ __device__ static constexpr uint32_t tO(int t) { return 256u + D * t; }
-    __host__ __device__ static constexpr uint32_t tP(int t) { return SEP ? 384u + 64u * t : tS(t); }
+    __host__ __device__ static constexpr uint32_t tS(int t) { return NB * HT * t; }
+    __host__ __device__ static constexpr uint32_t tO(int t) { return 2 * NB * HT + D * t; }
+    static_assert(2 * NB * HT + 2 * D <= 512, "tensor memory budget");
 };
 
 template <int D>
@@ -74,13 +80,15 @@ __global__ void __launch_bounds__(NTH, 1)
     if (at.seq < 0) return;
     const int h = blockIdx.x % Hq, hk = h / (Hq / Hk);
     const int q0 = at.block * 2 * BT, rows = at.len - q0;  // rows of this CTA's queries that exist
-    const int n0 = 2 * at.block + 1, n1 = rows > BT ? n0 + 1 : 0, nmax = n1 ? n1 : n0;  // key blocks per tile
+    // steps of the two tiles (the keys their rows see), and key tiles of 128
+    const int n0 = (min(at.len, q0 + BT) + HT - 1) / HT, n1 = rows > BT ? (min(at.len, q0 + 2 * BT) + HT - 1) / HT : 0;
+    const int tiles = (max(n0, n1) + 1) / 2;
 
     if (tid == 0) {
         for (int i = 0; i < C::NBAR; ++i) {
             int n = 1;
             if ((i >= C::k_empty && i < C::v_full) || (i >= C::v_empty && i < C::v_zeroed)) n = n1 ? 2 : 1;
-            if (i >= C::s_free && i < C::pv_done) n = BT / 32;  // one a warp
+            if (i >= C::p_full && i < C::pv_done) n = BT / 32;  // one a warp
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
@@ -105,7 +113,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 mbar_arrive_expect_tx(&bar[C::q_full + t], C::TILE);
                 load_tile<D>(sm + C::Q + t * C::TILE, &tmQ, &bar[C::q_full + t], h, (int)at.t0 + q0 + t * BT);
             }
-            for (int j = 0; j < nmax && !w.aborted(); ++j) {
+            for (int j = 0; j < tiles && !w.aborted(); ++j) {
                 const int s = j % NS;
                 if (j >= NS) w.wait(&bar[C::k_empty + s], j / NS - 1);
                 if (w.aborted()) break;
@@ -118,10 +126,10 @@ __global__ void __launch_bounds__(NTH, 1)
             }
         }
         __syncwarp();
-        const int last = at.len - (nmax - 1) * BT;
+        const int last = at.len - (tiles - 1) * BT;
         if (last < BT) {
-            const int s = (nmax - 1) % NS;
-            w.wait(&bar[C::v_full + s], (nmax - 1) / NS);
+            const int s = (tiles - 1) % NS;
+            w.wait(&bar[C::v_full + s], (tiles - 1) / NS);
             if (!w.stopped()) zero_rows<D>(sm + C::V + s * C::TILE, last, lane);
             if (lane == 0) arrive(&bar[C::v_zeroed]);
         }
@@ -130,43 +138,37 @@ __global__ void __launch_bounds__(NTH, 1)
         const int t = warp - 8, n = t ? n1 : n0;
         if (n > 0) {
             const unsigned char *qt = sm + C::Q + t * C::TILE;
-            const uint32_t tS = tmem + C::tS(t), tO = tmem + C::tO(t), tP = tmem + C::tP(t);
             auto scores = [&](int j) {
-                const int s = j % NS;
-                w.wait(&bar[C::k_full + s], j / NS);
+                const int k = j >> 1, s = k % NS, b = j % C::NB;
+                w.wait(&bar[C::k_full + s], k / NS);
                 tc_fence_after();
-                mma_nt<D>(tS, qt, sm + C::K + s * C::TILE);
-                commit(&bar[C::s_full + t]);
-                commit(&bar[C::k_empty + s]);
+                mma_nt<D, HT>(tmem + C::tS(t) + HT * b, qt, sm + C::K + s * C::TILE + (j & 1) * kHalf);
+                commit(&bar[C::s_full + C::NB * t + b]);
+                if ((j & 1) || j == n - 1) commit(&bar[C::k_empty + s]);
             };
             w.wait(&bar[C::q_full + t], 0);
-            scores(0);
+            for (int j = 0; j < C::NB && j < n; ++j) scores(j);
             for (int j = 0; j < n && !w.stopped(); ++j) {
-                const int s = j % NS;
-                if (C::SEP && j + 1 < n) {
-                    w.wait(&bar[C::s_free + t], j);
-                    scores(j + 1);
-                }
-                w.wait(&bar[C::v_full + s], j / NS);
-                if (j == nmax - 1 && at.len < nmax * BT) w.wait(&bar[C::v_zeroed], 0);
-                w.wait(&bar[C::p_half + 2 * t], j);
+                const int k = j >> 1, s = k % NS;
+                w.wait(&bar[C::v_full + s], k / NS);
+                if (k == tiles - 1 && at.len < tiles * BT) w.wait(&bar[C::v_zeroed], 0);
+                w.wait(&bar[C::p_full + C::NB * t + j % C::NB], j / C::NB);
                 tc_fence_after();
-                mma_tn<D>(tO, tP, sm + C::V + s * C::TILE, 0, 4, j > 0);
-                w.wait(&bar[C::p_half + 2 * t + 1], j);
-                tc_fence_after();
-                mma_tn<D>(tO, tP, sm + C::V + s * C::TILE, 4, 8, true);
-                commit(&bar[C::pv_done + t]);
-                commit(&bar[C::v_empty + s]);
-                if (!C::SEP && j + 1 < n) {  // the next S overwrites P
-                    w.wait(&bar[C::pv_done + t], j);
-                    scores(j + 1);
+                mma_tn<D>(tmem + C::tO(t), tmem + C::tS(t) + HT * (j % C::NB), sm + C::V + s * C::TILE + (j & 1) * kHalf, 0,
+                          HT / 16, j > 0);
+                commit(&bar[C::pv_done + 2 * t + (j & 1)]);
+                if ((j & 1) || j == n - 1) commit(&bar[C::v_empty + s]);
+                if (j + C::NB < n) {  // over P
+                    w.wait(&bar[C::pv_done + 2 * t + (j & 1)], j >> 1);
+                    scores(j + C::NB);
                 }
             }
-            if (t == 0 && n1) {  // tile 0 has no part in the last block
-                const int s = (nmax - 1) % NS;
-                w.wait(&bar[C::k_full + s], (nmax - 1) / NS);
+            commit(&bar[C::all_done + t]);
+            for (int k = (n + 1) / 2; k < tiles; ++k) {  // key tiles that this query tile has no part in
+                const int s = k % NS;
+                w.wait(&bar[C::k_full + s], k / NS);
                 if (lane == 0) arrive(&bar[C::k_empty + s]);
-                w.wait(&bar[C::v_full + s], (nmax - 1) / NS);
+                w.wait(&bar[C::v_full + s], k / NS);
                 if (lane == 0) arrive(&bar[C::v_empty + s]);
             }
             if (w.stopped()) {  // products issued already end before the tensor memory is freed
@@ -180,46 +182,43 @@ __global__ void __launch_bounds__(NTH, 1)
         // ---- softmax of tile t; thread = row ----
         const int t = warp >> 2, n = t ? n1 : n0, wq = warp & 3, r = tid & (BT - 1);
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
-        const uint32_t tS = tmem + lanes + C::tS(t), tO = tmem + lanes + C::tO(t), tP = tmem + lanes + C::tP(t);
-        float m = -INFINITY, l = 0.f;  // m in units of S
-        for (int j = 0; j < n; ++j) {
-            float s[4][32];
-            w.wait(&bar[C::s_full + t], j);
-            if (w.stopped()) break;
+        const uint32_t tS = tmem + lanes + C::tS(t), tO = tmem + lanes + C::tO(t);
+        const int jd = 2 * (2 * at.block + t);  // first step of the diagonal block
+        float m = -INFINITY, l = 0.f;           // m in units of S
+        auto fetch = [&](int j, float (&x)[2][32]) {
+            w.wait(&bar[C::s_full + C::NB * t + j % C::NB], j / C::NB);
             tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld32(tS + 32 * x, s[x]);
+            tmem_ld32(tS + HT * (j % C::NB), x[0]);
+            tmem_ld32(tS + HT * (j % C::NB) + 32, x[1]);
+        };
+        // step j, whose scores are s; those of the next step are fetched into `next`
+        auto step = [&](int j, float (&s)[2][32], float (&next)[2][32]) {
             tmem_wait_ld();
-            if (C::SEP) {
-                tc_fence_before();
-                warp_arrive(&bar[C::s_free + t], lane);
-            }
-            if (j == n - 1) {  // the diagonal block
+            if (j >= jd) {
+                const int c0 = HT * (j - jd);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (32 * x + i > r) s[x][i] = -INFINITY;
+                        if (c0 + 32 * x + i > r) s[x][i] = -INFINITY;
             }
-            float mx[4];
+            float mx[2];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 2; ++x) {
                 mx[x] = fmaxf(s[x][0], s[x][1]);
 #pragma unroll
                 for (int i = 2; i < 32; i += 2) mx[x] = max3(mx[x], s[x][i], s[x][i + 1]);
             }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (C::SEP && j > 0) {  // O is at rest, and the last P has been read
-                w.wait(&bar[C::pv_done + t], j - 1);
-                tc_fence_after();
-            }
+            const float top = fmaxf(mx[0], mx[1]);
             const bool move = (top - m) * scale2 > 8.f;  // also from -inf
             if (__any_sync(0xffffffffu, move)) {
                 const float to = move ? top : m;
                 const float f = move ? ex2_approx((m - to) * scale2) : 1.f;
                 m = to;
                 l *= f;
-                if (j > 0) {
+                if (j > 0) {  // once O is at rest
+                    w.wait(&bar[C::pv_done + 2 * t + ((j - 1) & 1)], (j - 1) >> 1);
+                    tc_fence_after();
 #pragma unroll
                     for (int x = 0; x < D / 32; ++x) {
                         float o[32];
@@ -234,35 +233,38 @@ __global__ void __launch_bounds__(NTH, 1)
             const float ms = m == -INFINITY ? 0.f : m * scale2;
             const uint64_t sc2 = pack2(scale2, scale2), ms2 = pack2(-ms, -ms);
             uint64_t sum[2] = {0, 0};
+            float p[32];  // 64 weights, two bf16 each
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float p[32];  // 64 weights, two bf16 each
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int c = 64 * hf + 2 * i;
-                    float a, b;
-                    unpack2(fma2(pack2(s[c >> 5][c & 31], s[c >> 5][(c & 31) + 1]), sc2, ms2), a, b);
-                    a = ex2_approx(a);
-                    b = ex2_approx(b);
-                    sum[i & 1] = add2(sum[i & 1], pack2(a, b));
-                    p[i] = __uint_as_float(pack_bf16x2(a, b));
-                }
-                tmem_st32(tP + 32 * hf, p);
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(&bar[C::p_half + 2 * t + hf], lane);
+            for (int i = 0; i < 32; ++i) {
+                float a, b;
+                unpack2(fma2(pack2(s[i >> 4][2 * (i & 15)], s[i >> 4][2 * (i & 15) + 1]), sc2, ms2), a, b);
+                a = ex2_approx(a);
+                b = ex2_approx(b);
+                sum[i & 1] = add2(sum[i & 1], pack2(a, b));
+                p[i] = __uint_as_float(pack_bf16x2(a, b));
             }
+            tmem_st32(tS + HT * (j % C::NB), p);
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bar[C::p_full + C::NB * t + j % C::NB], lane);
             float a, b;
             unpack2(add2(sum[0], sum[1]), a, b);
             l += a + b;
-        }
-        if (n > 0 && !w.stopped()) {
-            w.wait(&bar[C::pv_done + t], n - 1);
+            if (j + 1 < n) fetch(j + 1, next);
+        };
+        if (n > 0) {
+            float x[2][32], y[2][32];
+            fetch(0, x);
+            for (int j = 0; j < n && !w.stopped(); j += 2) {
+                step(j, x, y);
+                if (j + 1 < n) step(j + 1, y, x);
+            }
+            w.wait(&bar[C::all_done + t], 0);
             tc_fence_after();
             if (!w.stopped()) {
                 const int64_t row0 = at.t0 + q0 + t * BT;
-                store_rows<D, D>(tO, 1.f / l, sm + C::Q + t * C::TILE, wq, lane, 0, out + (row0 * Hq + h) * D, (int64_t)Hq * D,
-                              rows - t * BT);
+                store_rows<D, D>(tO, 1.f / l, sm + C::Q + t * C::TILE, wq, lane, 0, out + (row0 * Hq + h) * D,
+                                 (int64_t)Hq * D, rows - t * BT);
                 if (lse && r < rows - t * BT) lse[(row0 + r) * Hq + h] = fmaf(m, scale2, log2f(l)) * kLn2;
             }
         }
