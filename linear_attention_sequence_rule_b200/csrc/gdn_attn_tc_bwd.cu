@@ -25,8 +25,9 @@
 // are moved to tensor memory: Q and dO on the query side, K and V on the key side at d = 64 (at d = 128 there
 // is no room for them; with K there and one dP tile a step takes 1920 cycles, with two dP tiles 1640).
 //   warps 0-7, 8-15  element by element, the even and the odd steps: a thread has a row, 32 columns
-//   warps 16-18      issue the products
-//   warp 19          loads; zeroes rows behind the sequence's end
+//   warps 16-18      issue the products (key side: 16-19; one product a warp, since its waits and commits
+//                    take longer than the product)
+//   warp 19 (20)     loads; zeroes rows behind the sequence's end
 // P and dS (bf16) are written over the first half of the very S or dP columns they came from, which
 // their own thread has read.
 #include <math.h>
@@ -43,7 +44,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int NTH = 640;
+constexpr int NTH = 640, NTH_KEY = 768;
 constexpr int NEL = 512;         // threads of the element-wise warps
 constexpr int HT = 64;           // rows of the other side a step
 constexpr int kHalf = HT * 128;  // bytes from a tile's first half to its second (in each sub-tile)
@@ -192,8 +193,10 @@ __global__ void __launch_bounds__(NTH, 1)
             for (int p = 0, i = 0; p < passes; ++p)
                 for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
                     const int j = p * nt + (s >> 1);
-                    w.wait(&bar[C::k_full + j % NK], j / NK);
-                    if (rows < BT) w.wait(&bar[C::k_zeroed + j % NK], j / NK);
+                    if (!(s & 1)) {
+                        w.wait(&bar[C::k_full + j % NK], j / NK);
+                        if (rows < BT) w.wait(&bar[C::k_zeroed + j % NK], j / NK);
+                    }
                     if (i > 1) w.wait(&bar[C::s_free + (i & 1)], (i >> 1) - 1);
                     tc_fence_after();
                     mma_nt_ta<D, HT>(tmem + C::tS + HT * (i & 1), tmem + C::tQ, sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf);
@@ -204,8 +207,10 @@ __global__ void __launch_bounds__(NTH, 1)
             for (int p = 0, i = 0; p < passes; ++p)
                 for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
                     const int j = p * nt + (s >> 1);
-                    w.wait(&bar[C::v_full + j % NV], j / NV);
-                    if (rows < BT) w.wait(&bar[C::v_zeroed + j % NV], j / NV);
+                    if (!(s & 1)) {
+                        w.wait(&bar[C::v_full + j % NV], j / NV);
+                        if (rows < BT) w.wait(&bar[C::v_zeroed + j % NV], j / NV);
+                    }
                     if (i > 1) w.wait(&bar[C::dq_done + (i & 1)], (i >> 1) - 1);
                     tc_fence_after();
                     mma_nt_ta<D, HT>(tmem + C::tP + HT * (i & 1), tmem + C::tO, sm + C::V + (j % NV) * C::TILE + (s & 1) * kHalf);
@@ -354,7 +359,7 @@ template <int D> struct DkvCfg {
     static constexpr int kv_full = 0;
     static constexpr int q_full = 1;               // [NS] Q, and -lse log2 e and -D of its rows
     static constexpr int o_full = q_full + NS;     // [NS] dO
-    static constexpr int empty = o_full + NS;      // [NS] the stage has been used
+    static constexpr int empty = o_full + NS;      // [NS] dV and dK have used the stage
     static constexpr int zeroed = empty + NS;      // [NS] the stage has no row behind the end (ragged ends only)
     static constexpr int s_full = zeroed + NS;     // [2]
     static constexpr int dp_full = s_full + 2;     // [2]
@@ -364,8 +369,8 @@ template <int D> struct DkvCfg {
     static constexpr int dk_done = dv_done + 2;    // [2] dS^T has been used
     static constexpr int a_full = dk_done + 2;     // K (and V) are in tensor memory
     static constexpr int all_done = a_full + 1;    // dV and dK are there
-    static constexpr int drain = all_done + 1;     // [3]
-    static constexpr int NBAR = drain + 3;
+    static constexpr int drain = all_done + 1;     // [4]
+    static constexpr int NBAR = drain + 4;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
     static constexpr bool TA = D == 64;            // K and V in tensor memory
@@ -375,7 +380,7 @@ template <int D> struct DkvCfg {
 };
 
 template <int D>
-__global__ void __launch_bounds__(NTH, 1)
+__global__ void __launch_bounds__(NTH_KEY, 1)
     attn_bwd_dkv_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const float *__restrict__ nlse, const float *__restrict__ ndot, __nv_bfloat16 *__restrict__ dk,
@@ -410,12 +415,13 @@ __global__ void __launch_bounds__(NTH, 1)
             if (i >= C::q_full && i < C::o_full) c = 1 + 32;
             if (i >= C::p_full && i < C::dv_done) c = NEL / 64;  // one a warp
             if (i == C::a_full) c = NEL / 32;
+            if ((i >= C::empty && i < C::zeroed) || i == C::all_done) c = 2;  // dV and dK
             mbar_init(&bar[i], c);
         }
         fence_mbar_init();
         *abort_flag = 0;
     }
-    if (warp == 19) {
+    if (warp == 20) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -424,10 +430,11 @@ __global__ void __launch_bounds__(NTH, 1)
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-    // registers: as on the query side
+    // registers: 768 x 80 = 61440 at launch; 512 x 96 + 256 x 48 = 61440 after the roles' changes (warps
+    // 21-23 are there because registers are dealt out by four warps)
     if (warp >= 16) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 19) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 20) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bar[C::kv_full], 2 * C::TILE);
                 load_tile<D>(sm + C::K, &tmK, &bar[C::kv_full], hk, (int)row0);
@@ -470,8 +477,10 @@ __global__ void __launch_bounds__(NTH, 1)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
                     if (i > 1) w.wait(&bar[C::dv_done + (i & 1)], (i >> 1) - 1);
-                    w.wait(&bar[C::q_full + s], j / NS);
-                    if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
+                    if (!(x & 1)) {
+                        w.wait(&bar[C::q_full + s], j / NS);
+                        if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
+                    }
                     tc_fence_after();
                     if (C::TA)
                         mma_nt_ta<D, HT>(tmem + C::tS + HT * (i & 1), tmem + C::tK, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
@@ -485,8 +494,10 @@ __global__ void __launch_bounds__(NTH, 1)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
                     if (i > 1) w.wait(&bar[C::dk_done + (i & 1)], (i >> 1) - 1);
-                    w.wait(&bar[C::o_full + s], j / NS);
-                    if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
+                    if (!(x & 1)) {
+                        w.wait(&bar[C::o_full + s], j / NS);
+                        if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
+                    }
                     tc_fence_after();
                     if (C::TA)
                         mma_nt_ta<D, HT>(tmem + C::tP + HT * (i & 1), tmem + C::tV, sm + C::O + s * C::TILE + (x & 1) * kHalf);
@@ -494,30 +505,39 @@ __global__ void __launch_bounds__(NTH, 1)
                         mma_nt<D, HT>(tmem + C::tP + HT * (i & 1), sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
                     commit(&bar[C::dp_full + (i & 1)]);
                 }
-        } else {  // dV, dK
+        } else if (warp == 18) {  // dV
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
-                    const int j = g * nt + (x >> 1), s = j % NS, at_ = s * C::TILE + (x & 1) * kHalf;
-                    w.wait(&bar[C::o_full + s], j / NS);
-                    if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
+                    const int j = g * nt + (x >> 1), s = j % NS;
+                    if (!(x & 1)) {
+                        w.wait(&bar[C::o_full + s], j / NS);
+                        if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
+                    }
                     w.wait(&bar[C::p_full + (i & 1)], i >> 1);
                     tc_fence_after();
-                    mma_step<D>(tmem + C::tGV, tmem + C::tS + HT * (i & 1), sm + C::O + at_, i > 0);
+                    mma_step<D>(tmem + C::tGV, tmem + C::tS + HT * (i & 1), sm + C::O + s * C::TILE + (x & 1) * kHalf, i > 0);
                     commit(&bar[C::dv_done + (i & 1)]);
+                    if ((x & 1) || x == n - 1) commit(&bar[C::empty + s]);
+                }
+            commit(&bar[C::all_done]);
+        } else if (warp == 19) {  // dK
+            for (int g = 0, i = 0; g < G; ++g)
+                for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
+                    const int s = (g * nt + (x >> 1)) % NS;
                     w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
                     tc_fence_after();
-                    mma_step<D>(tmem + C::tGK, tmem + C::tP + HT * (i & 1), sm + C::Q + at_, i > 0);
+                    mma_step<D>(tmem + C::tGK, tmem + C::tP + HT * (i & 1), sm + C::Q + s * C::TILE + (x & 1) * kHalf, i > 0);
                     commit(&bar[C::dk_done + (i & 1)]);
                     if ((x & 1) || x == n - 1) commit(&bar[C::empty + s]);
                 }
             commit(&bar[C::all_done]);
         }
-        if (warp < 19 && w.stopped()) {  // products issued already end before the tensor memory is freed
+        if (warp < 20 && w.stopped()) {  // products issued already end before the tensor memory is freed
             commit(&bar[C::drain + warp - 16]);
             mbar_wait_bounded(&bar[C::drain + warp - 16], 0, 100000000ull);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         const int g = warp >> 2, wq = warp & 3, r = tid & (BT - 1);  // r: key row
         const int set = g >> 1, c0 = 32 * (g & 1);  // steps of this parity, these columns
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
@@ -593,13 +613,13 @@ __global__ void __launch_bounds__(NTH, 1)
             }
         }
     }
-    if (w.aborted() && warp == 19) {
+    if (w.aborted() && warp == 20) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (lane == 0) drain_loads(bar, C::kv_full, 1 + 2 * NS);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 19) {
+    if (warp == 20) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -623,7 +643,7 @@ template <int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t st)
     attn_bwd_dq_tc<D><<<(unsigned)(tiles * a.Hq), NTH, A::TOTAL, st>>>(
         mq, mk, mv, mo, static_cast<const __nv_bfloat16 *>(a.out), a.lse, static_cast<__nv_bfloat16 *>(a.dq), nlse, ndot,
         a.cu, a.B, a.T, a.Hq, a.Hk, a.scale, tokens);
-    attn_bwd_dkv_tc<D><<<(unsigned)(tiles * a.Hk), NTH, Bc::TOTAL, st>>>(
+    attn_bwd_dkv_tc<D><<<(unsigned)(tiles * a.Hk), NTH_KEY, Bc::TOTAL, st>>>(
         mq, mk, mv, mo, nlse, ndot, static_cast<__nv_bfloat16 *>(a.dk), static_cast<__nv_bfloat16 *>(a.dv), a.cu, a.B, a.T,
         a.Hq, a.Hk, a.scale, tokens);
     return cudaGetLastError();

@@ -12,10 +12,12 @@ struct AttnTile {
     int64_t t0;  // the sequence's first token
 };
 
-// Tile `index` of a launch over blocks of `rows` tokens, from last blocks to first ones (under the
-// causal mask the last query block has the most work): dense calls (B ceil(T / rows) tiles) block by
-// block over all sequences, packed ones (at most T / rows + B tiles; those past the last one are
-// empty) sequence by sequence.  Called by whole warps; 32 sequences are looked at at a time.
+// Tile `index` of a launch over blocks of `rows` tokens, the tiles with the most work first: block b of
+// a sequence attends to b + 1 blocks, so tiles go from the highest block down over all sequences, and the
+// launch does not end with a long one alone.  Dense calls have B ceil(T / rows) tiles; a packed launch
+// has at most T / rows + B, and the tiles past the last one are empty.  With more than 128 sequences
+// (each lane holds four lengths; many sequences of a launch's size are short ones) packed tiles go
+// sequence by sequence, each from its last block on.  Called by whole warps.
 __device__ __forceinline__ AttnTile attn_tile(const int32_t *__restrict__ cu, int B, int T, int rows, int index)
 {
     AttnTile r;
@@ -32,6 +34,44 @@ __device__ __forceinline__ AttnTile attn_tile(const int32_t *__restrict__ cu, in
     r.seq = -1;
     r.block = r.len = 0;
     r.t0 = 0;
+    if (B <= 128) {
+        int n[4], most = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int s = 32 * x + lane;
+            n[x] = 0;
+            if (s < B) {
+                const int a = cu[s], len = min(cu[s + 1], T) - a;
+                if (a >= 0 && len > 0) n[x] = (len + rows - 1) / rows;
+            }
+            most = max(most, n[x]);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        // tiles of block b and above: sum of max(0, n - b); the block sought is the highest with more than `index`
+        auto above = [&](int b) {
+            int c = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) c += max(0, n[x] - b);
+            return __reduce_add_sync(0xffffffffu, c);
+        };
+        if (index >= above(0)) return r;
+        int lo = 0, hi = most;  // above(lo) > index >= above(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (above(mid) > index) lo = mid; else hi = mid;
+        }
+        int k = index - above(lo + 1);  // among the sequences with a block lo, in their order
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const unsigned has = __ballot_sync(0xffffffffu, n[x] > lo);
+            if (r.seq < 0 && k < __popc(has)) r.seq = 32 * x + (int)__fns(has, 0, k + 1);
+            k -= __popc(has);
+        }
+        r.block = lo;
+        r.t0 = cu[r.seq];
+        r.len = min(cu[r.seq + 1], T) - (int)r.t0;
+        return r;
+    }
     for (int s0 = 0; s0 < B; s0 += 32) {
         const int s = s0 + lane;
         int a = 0, len = 0;
