@@ -190,20 +190,17 @@ __global__ void __cluster_dims__(PC, 1, 1) __launch_bounds__(PT) cache_plan_kern
 
 // ---- append ---------------------------------------------------------------------------------------
 //
-// One CTA takes the runs (rows of one page) that begin in its block of rows, for one head and for
-// keys or values: the largest magnitude of the run, the page's new scale 2^e, then the quotients.
-// Dividing by a power of two is exact, so a token that is held already changes only where it falls
-// into e4m3's subnormal range, and the plain form's values come out bit for bit.
+// A run is the rows of one page, for one head and for keys or values: the largest magnitude of its rows,
+// the page's new scale 2^e, then the quotients.  Dividing by a power of two is exact, so a token that is
+// held already changes only where it falls into e4m3's subnormal range, and the plain form's values
+// come out bit for bit.
+//
+// Memory bounds it: 2 or 4 bytes in and 1 out an element.  A CTA takes a block of rows for one head, keys
+// or values, and finds the runs that begin there: short ones (a generation step's, of one row) go to
+// groups of lanes as wide as a row, side by side; the rows of a long one (a prompt's) are held in the CTA's
+// registers between the maximum and the quotients, so that they are read once.
 
-constexpr int AT = 128;  // threads per CTA
-
-__device__ __forceinline__ float4 load_row4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load_row4(const __nv_bfloat16 *p)
-{
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xffff0000u));
-}
+constexpr int AT = 256;  // threads per CTA
 
 // The least power of two 2^e, e >= -60, with amax <= 448 x 2^e = 1.75 x 2^(e + 8).
 __device__ __forceinline__ float scale_of(float amax)
@@ -226,91 +223,217 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-__device__ __forceinline__ float absmax4(float m, float4 x)  // NaN is passed over
+// 16 bytes of a row: 8 bf16 or 4 fp32
+template <typename T> struct Vec16;
+template <> struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ float amax(float m) const
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xffff0000u))));
+        return m;
+    }
+    __device__ __forceinline__ void store(uint8_t *p, float f) const
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t r[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            r[i] = to_e4m3x4(make_float4(__uint_as_float(u[2 * i] << 16) * f, __uint_as_float(u[2 * i] & 0xffff0000u) * f,
+                                         __uint_as_float(u[2 * i + 1] << 16) * f,
+                                         __uint_as_float(u[2 * i + 1] & 0xffff0000u) * f));
+        *reinterpret_cast<uint2 *>(p) = make_uint2(r[0], r[1]);
+    }
+};
+template <> struct Vec16<float> {
+    static constexpr int N = 4;
+    float4 w;
+    __device__ __forceinline__ void load(const float *p) { w = __ldcs(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ float amax(float m) const
+    {
+        return fmaxf(fmaxf(m, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(w.z), fabsf(w.w)));
+    }
+    __device__ __forceinline__ void store(uint8_t *p, float f) const
+    {
+        *reinterpret_cast<uint32_t *>(p) = to_e4m3x4(make_float4(w.x * f, w.y * f, w.z * f, w.w * f));
+    }
+};
+
+// Held values of a page after its scale has grown by 1 / f: E bytes from p on in rows r0, r0 + STEP, ...
+// below n, eight rows under way at a time.
+template <int D, int E, int STEP> __device__ __forceinline__ void shrink_rows(uint8_t *p, int r0, int n, float f)
 {
-    return fmaxf(fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+    for (int r = r0; r < n; r += 8 * STEP) {
+        uint32_t w[8][E / 4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e)
+                if (r + i * STEP < n) w[i][e] = *reinterpret_cast<const uint32_t *>(p + (r + i * STEP) * D + 4 * e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e)
+                if (r + i * STEP < n) {
+                    const float2 lo = from_e4m3x2(w[i][e]), hi = from_e4m3x2(w[i][e] >> 16);
+                    *reinterpret_cast<uint32_t *>(p + (r + i * STEP) * D + 4 * e) =
+                        to_e4m3x4(make_float4(lo.x * f, lo.y * f, hi.x * f, hi.y * f));
+                }
+    }
 }
 
+struct Where {
+    int shift, nslots;
+    __device__ __forceinline__ bool on(int slot) const { return slot >= 0 && slot < nslots; }
+    // does a row with slot `b` continue the run of the row before it, with slot `a`?
+    __device__ __forceinline__ bool same_page(int a, int b) const { return on(a) && on(b) && (a >> shift) == (b >> shift); }
+};
+
+// A run of n rows from x on, by a group of C = D / E lanes (lane c of it, the others in `group`).
 template <typename T, int D>
-__global__ void __launch_bounds__(AT) cache_append_kernel(const T *__restrict__ k, const T *__restrict__ v,
+__device__ __forceinline__ void append_run(const T *x, int64_t ld, uint8_t *base, float *scale, int n, int off, int c,
+                                           uint32_t group)
+{
+    constexpr int E = Vec16<T>::N, C = D / E;
+    const float was = off ? *scale : 0.f;
+    Vec16<T> y;
+    float mx = 0.f;
+    for (int r = n - 1; r >= 0; --r) {
+        y.load(x + r * ld);
+        mx = y.amax(mx);
+    }
+#pragma unroll
+    for (int o = C / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, o));
+    const float to = fmaxf(was, scale_of(mx)), inv = 1.f / to;
+    if (off && to != was) shrink_rows<D, E, 1>(base, 0, off, was * inv);
+    y.store(base + off * D, inv);  // the run's first row is the last one read
+    for (int r = 1; r < n; ++r) {  // the others again, from L2
+        y.load(x + r * ld);
+        y.store(base + (off + r) * D, inv);
+    }
+    __syncwarp(group);  // every lane has the old scale
+    if (c == 0) *scale = to;
+}
+
+// Loads of 16 bytes a thread that hold a page's rows of one head in a CTA's registers.
+template <typename T, int D, int PAGE> constexpr int NPB = (PAGE * (D / Vec16<T>::N) + AT - 1) / AT;
+
+template <typename T, int D, int PAGE, int TILE>
+__global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append_kernel(const T *__restrict__ k, const T *__restrict__ v,
                                                           const int32_t *__restrict__ slots, uint8_t *k_cache,
                                                           uint8_t *v_cache, float *k_scale, float *v_scale, int rows,
-                                                          int Hk, int page, int num_pages, int tile)
+                                                          int Hk, int num_pages)
 {
-    constexpr int C = D / 4;            // threads per row, four elements each
-    constexpr int RP = AT / C;          // rows at a time
+    constexpr int E = Vec16<T>::N, C = D / E, RP = AT / C;  // threads a row, rows at a time
+    constexpr int NP = NPB<T, D, PAGE>;                     // registers: NP x 16 bytes
     __shared__ float s_max[AT / 32];
-    const int tid = threadIdx.x, c = tid % C, rr = tid / C;
-    const int h = blockIdx.y;
-    const T *x = blockIdx.z ? v : k;
+    constexpr int kShortRun = 4;                            // up to this length a run goes to a group of lanes
+    constexpr int SPAN = (TILE + PAGE + 31) & ~31;          // rows looked at
+    static_assert(SPAN <= AT, "one row a thread");
+    __shared__ uint32_t s_lead[SPAN / 32], s_cont[SPAN / 32];
+    __shared__ int s_slot[TILE];
+    const int tid = threadIdx.x, lane = tid & 31, c = tid % C, rr = tid / C;
+    const int h = blockIdx.y, tile0 = blockIdx.x * TILE;
+    const T *x = (blockIdx.z ? v : k) + (int64_t)h * D + E * c;
     uint8_t *cache = blockIdx.z ? v_cache : k_cache;
     float *scale = blockIdx.z ? v_scale : k_scale;
     const int64_t ld = (int64_t)Hk * D;
-    const int shift = __ffs(page) - 1;
-    const int nslots = num_pages << shift;
-    const int t_end = min((int)(blockIdx.x + 1) * tile, rows);
-    for (int t = blockIdx.x * tile; t < t_end;) {
-        const int slot = slots[t];
-        const bool on = slot >= 0 && slot < nslots;
-        const int pg = slot >> shift, off = slot & (page - 1);
-        if (!on) {
-            ++t;
-            continue;
+    constexpr int shift = PAGE == 16 ? 4 : PAGE == 32 ? 5 : PAGE == 64 ? 6 : 7;
+    const Where w{shift, num_pages << shift};
+    // rows of this block and a page's worth behind it: which begin a run, which continue the row before them
+    if (tid < SPAN) {
+        const int t = tile0 + tid;
+        const int s = t < rows ? slots[t] : -1, before = t > 0 && t <= rows ? slots[t - 1] : -1;
+        const bool paged = w.same_page(before, s);
+        const uint32_t lead = __ballot_sync(0xffffffffu, w.on(s) && !paged && tid < TILE);
+        const uint32_t cont = __ballot_sync(0xffffffffu, paged && s == before + 1);
+        if (lane == 0) {
+            s_lead[tid >> 5] = lead;
+            s_cont[tid >> 5] = cont;
         }
-        if (t > 0) {  // rows of a run that began before this one
-            const int before = slots[t - 1];
-            if (before >= 0 && before < nslots && (before >> shift) == pg) {
-                ++t;
-                continue;
-            }
-        }
-        // the run: at most to the page's end
-        int n = 1;
-        while (off + n < page && t + n < rows && slots[t + n] == slot + n) ++n;
-        const T *xr = x + (int64_t)t * ld + (int64_t)h * D + 4 * c;
-        float mx = 0.f;
-        for (int r = rr; r < n; r += RP) mx = absmax4(mx, load_row4(xr + (int64_t)r * ld));
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if ((tid & 31) == 0) s_max[tid >> 5] = mx;
-        const int64_t ph = (int64_t)pg * Hk + h;
-        const float was = off ? scale[ph] : 0.f;
-        __syncthreads();
-        mx = s_max[0];
-#pragma unroll
-        for (int w = 1; w < AT / 32; ++w) mx = fmaxf(mx, s_max[w]);
-        const float to = fmaxf(was, scale_of(mx)), inv = 1.f / to;
-        uint8_t *base = cache + ((ph << shift)) * D + 4 * c;
-        if (off && to != was) {
-            const float f = was * inv;
-            for (int r = rr; r < off; r += RP) {
-                uint32_t *w = reinterpret_cast<uint32_t *>(base + r * D);
-                const uint32_t old = *w;
-                const float2 lo = from_e4m3x2(old), hi = from_e4m3x2(old >> 16);
-                *w = to_e4m3x4(make_float4(lo.x * f, lo.y * f, hi.x * f, hi.y * f));
-            }
-        }
-        for (int r = rr; r < n; r += RP) {
-            const float4 y = load_row4(xr + (int64_t)r * ld);
-            *reinterpret_cast<uint32_t *>(base + (off + r) * D) =
-                to_e4m3x4(make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-        }
-        __syncthreads();  // s_max is read, and every thread has the old scale
-        if (tid == 0) scale[ph] = to;
-        t += n;
+        if (tid < TILE) s_slot[tid] = s;
     }
+    __syncthreads();
+    auto leads = [&](int at) { return (s_lead[at >> 5] >> (at & 31)) & 1; };
+    auto length = [&](int at) {  // of the run that begins at row `at`: up to the first row that does not continue
+        int n = 1;
+        for (int i = at + 1; i < SPAN;) {
+            const uint32_t gap = ~s_cont[i >> 5] >> (i & 31);
+            const int more = gap ? __ffs(gap) - 1 : 32 - (i & 31);
+            n += more;
+            i += more;
+            if (gap) break;
+        }
+        return min(n, PAGE - (s_slot[at] & (PAGE - 1)));
+    };
+    const uint32_t group = (C == 32 ? 0xffffffffu : (1u << C) - 1) << (lane / C * C);
+    for (int at = rr; at < TILE; at += RP) {
+        if (!leads(at)) continue;
+        const int n = length(at);
+        if (n > kShortRun) continue;
+        const int slot = s_slot[at];
+        const int64_t ph = (int64_t)(slot >> shift) * Hk + h;
+        append_run<T, D>(x + (int64_t)(tile0 + at) * ld, ld, cache + (ph << shift) * D + E * c, scale + ph, n,
+                         slot & (PAGE - 1), c, group);
+    }
+    if (!__syncthreads_or(tid < TILE && leads(tid) && length(tid) > kShortRun)) return;
+    for (int q = 0; q < (TILE + 31) / 32; ++q)
+        for (uint32_t left = s_lead[q]; left; left &= left - 1) {
+            const int at = 32 * q + __ffs(left) - 1, t = tile0 + at, n = length(at);
+            if (n <= kShortRun) continue;
+            const int slot = s_slot[at], pg = slot >> shift, off = slot & (PAGE - 1);
+            const T *xr = x + (int64_t)t * ld;
+            Vec16<T> y[NP];
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                if (rr + RP * i < n) y[i].load(xr + (int64_t)(rr + RP * i) * ld);
+            const int64_t ph = (int64_t)pg * Hk + h;
+            const float was = off ? scale[ph] : 0.f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                if (rr + RP * i < n) mx = y[i].amax(mx);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (lane == 0) s_max[tid >> 5] = mx;
+            __syncthreads();
+            mx = s_max[0];
+#pragma unroll
+            for (int i = 1; i < AT / 32; ++i) mx = fmaxf(mx, s_max[i]);
+            const float to = fmaxf(was, scale_of(mx)), inv = 1.f / to;
+            uint8_t *base = cache + (ph << shift) * D + E * c;
+            if (off && to != was) shrink_rows<D, E, RP>(base, rr, off, was * inv);
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                if (rr + RP * i < n) y[i].store(base + (off + rr + RP * i) * D, inv);
+            __syncthreads();  // s_max is read, and every thread has the old scale
+            if (tid == 0) scale[ph] = to;
+        }
+}
+
+template <typename T, int D, int PAGE> cudaError_t run_append(const CacheAppendArgs &a, cudaStream_t st)
+{
+    // Rows a CTA: few where rows are few, so that a generation step's spread over the SMs (256 rows of 4 heads,
+    // d 128, page 64, bf16: 2.5 us with 16, 5.3 with 64), more where they are many (prompts of 32768 rows, d 64:
+    // 30 us with 16, 19 with 64, for 7.8 at the copy rate).
+    const int tile = a.rows <= 2048 ? 16 : 64;
+    auto kern = tile == 16 ? cache_append_kernel<T, D, PAGE, 16> : cache_append_kernel<T, D, PAGE, 64>;
+    kern<<<dim3((a.rows + tile - 1) / tile, a.Hk, 2), AT, 0, st>>>((const T *)a.k, (const T *)a.v, a.slots, a.k_cache,
+                                                                   a.v_cache, a.k_scale, a.v_scale, a.rows, a.Hk,
+                                                                   a.num_pages);
+    return cudaGetLastError();
 }
 
 template <typename T, int D> cudaError_t run_append(const CacheAppendArgs &a, cudaStream_t st)
 {
-    // rows per CTA: one where there are few (a generation step: every row is a run of its own), up
-    // to a page where there are many (prompts: one run per page), with about 16 CTAs per SM
-    const long want = (long)a.rows * a.Hk * 2 / (148 * 16);
-    const int tile = (int)(want < 1 ? 1 : want > a.page ? a.page : want);
-    const dim3 grid((a.rows + tile - 1) / tile, a.Hk, 2);
-    cache_append_kernel<T, D><<<grid, AT, 0, st>>>((const T *)a.k, (const T *)a.v, a.slots, a.k_cache, a.v_cache,
-                                                   a.k_scale, a.v_scale, a.rows, a.Hk, a.page, a.num_pages, tile);
-    return cudaGetLastError();
+    if (a.page == 16) return run_append<T, D, 16>(a, st);
+    if (a.page == 32) return run_append<T, D, 32>(a, st);
+    if (a.page == 64) return run_append<T, D, 64>(a, st);
+    return run_append<T, D, 128>(a, st);
 }
 
 }  // namespace
