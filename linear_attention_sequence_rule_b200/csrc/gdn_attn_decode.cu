@@ -36,7 +36,10 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int TT = 32;    // tokens per tile
 constexpr int NW = 4;     // warps per CTA
-constexpr int NSTG = 3;   // ring stages per warp
+constexpr int NSTG = 2;   // ring stages per warp
+constexpr int OCC = 3;    // CTAs per SM: while one starts (a chain of dependent loads) the others stream (256 ragged
+                          // contexts: 379 us; with two CTAs of three stages 396)
+constexpr int JW = 16;    // warps of the join
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -118,7 +121,7 @@ template <int D> __host__ __device__ constexpr int decode_smem()
 
 // F32: q as a sum of two fp16 in rows g and g + 8 (8 heads per tile), the weights likewise.
 template <int D, bool F32>
-__global__ void __launch_bounds__(NW * 32, 2)
+__global__ void __launch_bounds__(NW * 32, OCC)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const AttnDecodeArgs a, int splits, int mtiles)
 {
@@ -198,10 +201,7 @@ __global__ void __launch_bounds__(NW * 32, 2)
             pg0 = npg0, pg1 = npg1;
             ks0 = nks0, ks1 = nks1, vs0 = nvs0, vs1 = nvs1;
         }
-        if (at == 8) fetch_pages(i - 8 + 32, npg0, npg1);
-        if (at == 20) fetch_scales(npg0, npg1, nks0, nks1, nvs0, nvs1);
         const int p0 = max(__shfl_sync(0xffffffffu, pg0, at), 0), p1 = max(__shfl_sync(0xffffffffu, pg1, at), 0);
-        if (lane == at) info[i % NSTG] = TileInfo{ks0, ks1, vs0, vs1};
         if (lane == 0) {
             unsigned char *st = ring + (i % NSTG) * stage_bytes<D>();
             uint64_t *b = &bar[i % NSTG];
@@ -216,10 +216,18 @@ __global__ void __launch_bounds__(NW * 32, 2)
             }
         }
     };
+    // The scales of tile i, behind its loads: they come from memory as its bytes do.
+    auto note = [&](int i) {
+        const int at = i & 31;
+        if (lane == at) info[i % NSTG] = TileInfo{ks0, ks1, vs0, vs1};
+        if (at == 8) fetch_pages(i - 8 + 32, npg0, npg1);
+        if (at == 20) fetch_scales(npg0, npg1, nks0, nks1, nvs0, nvs1);
+    };
     fetch_pages(0, pg0, pg1);
-    fetch_scales(pg0, pg1, ks0, ks1, vs0, vs1);
     int issued = 0;
     for (; issued < NSTG && issued < mine; ++issued) load(issued);
+    fetch_scales(pg0, pg1, ks0, ks1, vs0, vs1);
+    for (int i = 0; i < issued; ++i) note(i);
     __syncwarp();
 
     // ---- q as A fragments; thread (g, c) holds rows g and g + 8 and, at k step ks, the four d values
@@ -429,7 +437,10 @@ __global__ void __launch_bounds__(NW * 32, 2)
         }
         if (partial) fence_proxy_async_smem();  // the zeros, before the stage's next bytes
         __syncwarp();                           // every lane has read the stage
-        if (issued < mine) load(issued++);
+        if (issued < mine) {
+            load(issued);
+            note(issued++);
+        }
         __syncwarp();
     }
     if (dead)  // copies in flight end before the CTA does
@@ -499,13 +510,13 @@ __global__ void __launch_bounds__(NW * 32, 2)
 }
 
 // Joins the splits of one (request, query head): out = sum_s e_s o_s / sum_s e_s l_s, e_s =
-// exp2(m_s - max m).  One CTA a row; warp w takes splits w, w + 4, ...
+// exp2(m_s - max m).  One CTA a row; warp w takes splits w, w + JW, ...
 template <int D, bool F32>
-__global__ void __launch_bounds__(NW * 32) attn_decode_join(const AttnDecodeArgs a, int splits)
+__global__ void __launch_bounds__(JW * 32) attn_decode_join(const AttnDecodeArgs a, int splits)
 {
     constexpr int E = D / 32;  // elements of a row per lane
-    __shared__ float s_o[NW][D];
-    __shared__ float2 s_ml[NW];
+    __shared__ float s_o[JW][D];
+    __shared__ float s_l[JW];
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int len = context_len(a.lens, (int)(row / a.Hq), a.max_blocks, a.page);
@@ -521,7 +532,7 @@ __global__ void __launch_bounds__(NW * 32) attn_decode_join(const AttnDecodeArgs
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
-    for (int s = warp; s < used; s += NW) {
+    for (int s = warp; s < used; s += JW) {
         const float *w = ws + (int64_t)s * (D + 4);
         const float2 ml = *reinterpret_cast<const float2 *>(w + D);
         const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
@@ -531,17 +542,16 @@ __global__ void __launch_bounds__(NW * 32) attn_decode_join(const AttnDecodeArgs
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = o[e];
-    if (lane == 0) s_ml[warp].y = L;
+    if (lane == 0) s_l[warp] = L;
     __syncthreads();
     if (threadIdx.x < D / 4) {
-        const int d0 = 4 * threadIdx.x;
+        const int d0 = 4 * threadIdx.x, n = min(used, JW);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         L = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
+        for (int w = 0; w < n; ++w) {
             const float4 y = *reinterpret_cast<const float4 *>(&s_o[w][d0]);
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-            L += s_ml[w].y;
+            L += s_l[w];
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         store_out<F32>(a.out, row * D + d0, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
@@ -560,19 +570,21 @@ int sm_count()
 
 int head_tiles(int G, int dtype) { return (G + (dtype == GDN_DTYPE_F32 ? 8 : 16) - 1) / (dtype == GDN_DTYPE_F32 ? 8 : 16); }
 
-// Splits of a context: enough CTAs for two per SM where there are few (request, key head) pairs, and
-// no split longer than 2048 tokens where contexts can be long (so that the longest contexts of a
-// ragged batch do not end the launch alone), but at least two tiles a warp.
+// Splits of a context.  A CTA starts with a chain of dependent loads, some 5 us, so splits beyond need cost:
+// - few (request, key head) pairs: one CTA for each place on the SMs, down to a tile a warp (one context of
+//   65536 tokens, 4 key heads: 22.8 us in 64 or 111 splits, 31 in 32, 27 in 255; of 4096: 7.9 us in 32
+//   splits, 8.9 in 16);
+// - more: about 2.3 for each place, so that the longest contexts of a ragged batch do not end the launch
+//   alone, down to two tiles a warp (contexts of 128 to 8192 tokens, 8 key heads: 16 of them 43 us in 8
+//   splits, 63 in 2; 256 of them 379 unsplit, 403 in 2).
 int split_count(int N, int Hk, int mtiles, int page, int max_blocks)
 {
     const long tiles = ((long)max_blocks * page + TT - 1) / TT;
-    const long units = (long)N * Hk * mtiles;
-    long s = (2L * sm_count() + units - 1) / units;
-    const long by_len = (tiles + 63) / 64;
-    if (s < by_len) s = by_len < 8 ? by_len : (s > 8 ? s : 8);
-    const long most = tiles / (2 * NW);
-    if (s > most) s = most;
-    return (int)(s < 1 ? 1 : s);
+    const long units = (long)N * Hk * mtiles, places = (long)OCC * sm_count();
+    const bool few = units * 16 <= places;
+    const long s = few ? places / units : (23 * places / 10 + units - 1) / units;
+    const long most = few ? tiles / NW : tiles / (2 * NW);
+    return (int)(s > most ? (most < 1 ? 1 : most) : (s < 1 ? 1 : s));
 }
 
 bool cache_map(CUtensorMap *m, const void *base, int num_pages, int Hk, int page, int d)
@@ -605,7 +617,7 @@ template <int D, bool F32> cudaError_t run_decode(const AttnDecodeArgs &a, cudaS
     // the join's CTAs may be set up while the last ones above run; they wait for all of them
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.N * a.Hq));
-    cfg.blockDim = dim3(NW * 32);
+    cfg.blockDim = dim3(JW * 32);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
