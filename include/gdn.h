@@ -470,6 +470,9 @@ GDN_API int gdn_cache_plan(const int32_t *lens, const int32_t *added, int32_t *b
  * even.  Infinities are stored as the largest finite value, NaN as NaN.  Offsets after the new rows
  * and pages not touched are left as they were.  d in {64, 128}, page in {16, 32, 64, 128},
  * num_pages page < 2^31; rows = 0 does nothing.  No workspace.
+ * A row on the page of the row before it that does not have the next slot is not written, nor are the
+ * rows behind it on that page (a slot given twice keeps its first row).  Rows of one page in two places
+ * of a call leave that page and its scale undefined; no other page is touched.
  */
 GDN_API int gdn_cache_append(const void *k, const void *v, const int32_t *slots, void *k_cache, void *v_cache,
                              float *k_scale, float *v_scale, int rows, int Hk, int d, int page, int num_pages,
@@ -484,8 +487,8 @@ GDN_API int gdn_cache_append(const void *k, const void *v, const int32_t *slots,
  * A request of length <= 0 gets zeros; lengths beyond max_blocks page are cut there; tokens whose
  * table entry is outside 0 .. num_pages - 1 are left out.  Cache contents beyond a request's length
  * are never part of a result, whatever they are.  Cached values enter the tensor cores as fp16
- * (exact), q as fp16 after a power-of-two scaling (bf16 exact over 22 binary orders; fp32 as a sum
- * of two fp16), softmax weights as fp16 (bf16 calls) or a sum of two fp16 (fp32 calls), sums in
+ * (exact), q as fp16 after a power-of-two scaling of each head (bf16 exact over 22 binary orders;
+ * fp32 as a sum of two fp16), softmax weights as fp16 (bf16 calls) or a sum of two fp16 (fp32 calls), sums in
  * fp32.  d in {64, 128}; scale finite and > 0.  Workspace: gdn_attn_decode_workspace_bytes(...)
  * bytes, 256-byte aligned (long contexts are split over CTAs; may be NULL when that is 0).
  */

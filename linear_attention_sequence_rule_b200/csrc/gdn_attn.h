@@ -31,6 +31,7 @@ int read_and_clear_attn_bwd_error();
 // fp32 on CUDA cores (gdn_attn_simt.cu).
 cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t stream);
 cudaError_t launch_attn_bwd_simt(const AttnArgs &a, cudaStream_t stream);
+size_t attn_bwd_simt_workspace(int B, int T, int Hq, int Hk, int d, int varlen);
 
 struct CachePlanArgs {
     const int32_t *lens, *added;

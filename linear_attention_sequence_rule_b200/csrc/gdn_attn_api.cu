@@ -109,9 +109,10 @@ int gdn_attn_fwd(const void *q, const void *k, const void *v, void *out, float *
 size_t gdn_attn_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d, int varlen, int dtype)
 {
     if (check_prompt("gdn_attn_bwd", B, T, Hq, Hk, d, varlen, dtype) != GDN_OK) return (size_t)-1;
-    // D of every (token, query head); bf16: -lse log2 e too
+    // bf16: D and -lse log2 e of every (token, query head)
     const size_t rows = (varlen ? (size_t)T : (size_t)B * T) * Hq;
-    return (rows * (dtype == GDN_DTYPE_BF16 ? 2 : 1) * sizeof(float) + 255) & ~(size_t)255;
+    const size_t bytes = dtype == GDN_DTYPE_BF16 ? 2 * rows * sizeof(float) : attn_bwd_simt_workspace(B, T, Hq, Hk, d, varlen);
+    return (bytes + 255) & ~(size_t)255;
 }
 
 int gdn_attn_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse, const void *dout,

@@ -233,13 +233,13 @@ __global__ void __launch_bounds__(NW * 32, OCC)
     // ---- q as A fragments; thread (g, c) holds rows g and g + 8 and, at k step ks, the four d values
     // of its 16-byte chunks of a K row: chunk 2c + i (D = 128) or c (D = 64), word e, ks = 4 i + e ----
     uint32_t qa[KS][4];
-    float unscale;  // score = accumulated x unscale x ks
+    float unscale0, unscale1;  // score = accumulated x unscale x ks, rows g and g + 8
     {
         const int h0 = mt * MH + g, h1 = F32 ? h0 : h0 + 8;
         const bool on0 = h0 < G, on1 = h1 < G;
         const int64_t r0 = ((int64_t)n * a.Hq + hk * G + h0) * D, r1 = ((int64_t)n * a.Hq + hk * G + h1) * D;
         float x0[KS][4], x1[KS][4];
-        float mx = 0.f;
+        float mx0 = 0.f, mx1 = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const int d0 = 16 * (D == 128 ? 2 * c + (ks >> 2) : c) + 4 * (ks & 3);
@@ -265,22 +265,32 @@ __global__ void __launch_bounds__(NW * 32, OCC)
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(x0[ks][j]), fabsf(x1[ks][j])));
+            for (int j = 0; j < 4; ++j) {
+                mx0 = fmaxf(mx0, fabsf(x0[ks][j]));
+                mx1 = fmaxf(mx1, fabsf(x1[ks][j]));
+            }
         }
-        // one power of two for the tile's rows brings the largest |q| into [256, 512): fp16 then
-        // holds values down to 2^-22 of it with full precision
+        // a power of two for each head brings its largest |q| into [256, 512): fp16 then holds values down
+        // to 2^-22 of it with full precision, whatever the other heads hold
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int e = mx > 0.f ? (int)(__float_as_uint(mx) >> 23) - 127 - 8 : 0;
-        const int ec = max(-126, min(e, 126));
-        const float down = __uint_as_float((uint32_t)(127 - ec) << 23);
-        unscale = __uint_as_float((uint32_t)(127 + ec) << 23) * a.scale * kLog2e;
+        for (int o = 1; o < 4; o <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        }
+        auto exponent = [](float mx) {
+            return mx > 0.f ? max(-126, min((int)(__float_as_uint(mx) >> 23) - 127 - 8, 126)) : 0;
+        };
+        auto two_to = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
+        const int e0 = exponent(mx0), e1 = exponent(mx1);
+        const float down0 = two_to(-e0), down1 = two_to(-e1);
+        unscale0 = two_to(e0) * a.scale * kLog2e;
+        unscale1 = two_to(e1) * a.scale * kLog2e;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                x0[ks][j] *= down;
-                x1[ks][j] *= down;
+                x0[ks][j] *= down0;
+                x1[ks][j] *= down1;
             }
             if (F32) {  // row g + 8: what fp16 rounding of row g left over
 #pragma unroll
@@ -348,12 +358,12 @@ __global__ void __launch_bounds__(NW * 32, OCC)
             }
         }
         // ---- softmax weights ----
-        const float fA = unscale * kA, fB = unscale * ksB;
+        const float fA = unscale0 * kA, fB = unscale0 * ksB, hA = unscale1 * kA, hB = unscale1 * ksB;
         const float lgA = onA ? log2f(vA) : 0.f, lgB = onB ? log2f(vsB) : 0.f;
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float f = j < 2 ? fA : fB, lg = j < 2 ? lgA : lgB;
+            const float f = j < 2 ? fA : fB, h = j < 2 ? hA : hB, lg = j < 2 ? lgA : lgB;
             const bool onj = j < 2 ? onA : onB;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -363,7 +373,7 @@ __global__ void __launch_bounds__(NW * 32, OCC)
                     s[j][e] = on ? fmaf(x, f, lg) : -INFINITY;
                 } else {
                     s[j][e] = on ? fmaf(s[j][e], f, lg) : -INFINITY;
-                    s[j][e + 2] = on ? fmaf(s[j][e + 2], f, lg) : -INFINITY;
+                    s[j][e + 2] = on ? fmaf(s[j][e + 2], h, lg) : -INFINITY;
                     mx1 = fmaxf(mx1, s[j][e + 2]);
                 }
                 mx0 = fmaxf(mx0, s[j][e]);

@@ -6,8 +6,10 @@
 //     s = scale q k^T,  m' = max(m, max_j s),  p = exp(s - m'),
 //     l' = l exp(m - m') + sum_j p,  o' = o exp(m - m') + p v,     out = o / l,  lse = m + log l.
 // Backward: two launches after D_i = dout_i . out_i.  The query side forms dq per query block over
-// its key blocks; the key side forms dk, dv per key block over the query heads that share it and
-// their query blocks, so that every gradient is summed by one CTA in one order.
+// its key blocks; the key side forms dk, dv per key block and query head over the head's query blocks, and
+// a last launch adds up the heads that share a key head, in order: every gradient is summed in one
+// order.  (One CTA for all heads that share a key block would need no last launch, but has few and long
+// CTAs: 1024 tokens, 4 heads on 1, d 64: 760 us against 283; 2 x 4096, 12 on 4: 6.18 ms against 5.53.)
 //
 // Tiles sit in shared memory in fp32 (rows of D + 4 floats: a quarter warp's float4 reads of 8
 // rows hit 8 different bank groups).  256 threads as 16 x 16; a thread holds RPT rows (ty RPT + i)
@@ -46,6 +48,23 @@ __device__ __forceinline__ void load_tile(float *s, const float *g, int64_t ld, 
         *reinterpret_cast<float4 *>(s + r * (D + 4) + 4 * c) = x;
     }
 }
+
+// The same by cp.async; the caller commits and waits.
+template <int ROWS, int D>
+__device__ __forceinline__ void load_tile_async(float *s, const float *g, int64_t ld, int r0, int len)
+{
+    constexpr int C = D / 4;
+#pragma unroll
+    for (int i = threadIdx.x; i < ROWS * C; i += NT) {
+        const int r = i / C, c = i % C;
+        const bool on = r0 + r < len;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(s + r * (D + 4) + 4 * c)),
+                     "l"(g + (int64_t)(on ? r0 + r : 0) * ld + 4 * c), "r"(on ? 16 : 0)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c)
 {
@@ -136,7 +155,7 @@ __device__ __forceinline__ float row_sum16(float x)
 // BM = 16 RPT query rows.
 template <int D, int RPT> constexpr int fwd_smem()
 {
-    return ((16 * RPT + 2 * BN) * (D + 4) + 16 * RPT * LDP) * 4;
+    return ((16 * RPT + 4 * BN) * (D + 4) + 16 * RPT * LDP) * 4;
 }
 
 template <int D, int RPT>
@@ -147,7 +166,8 @@ __global__ void __launch_bounds__(NT) attn_fwd_simt(const float *__restrict__ q,
 {
     constexpr int BM = 16 * RPT;
     extern __shared__ float sm[];
-    float *Qs = sm, *Ks = Qs + BM * (D + 4), *Vs = Ks + BN * (D + 4), *Ps = Vs + BN * (D + 4);
+    constexpr int TS = BN * (D + 4);
+    float *Qs = sm, *KV = Qs + BM * (D + 4), *Ps = KV + 4 * TS;  // K, V of this block and of the next
     const AttnTile t = attn_tile(cu, B, Tn, BM, blockIdx.x);
     if (t.seq < 0) return;
     const int h = blockIdx.y, hk = h / (Hq / Hk);
@@ -166,10 +186,18 @@ __global__ void __launch_bounds__(NT) attn_fwd_simt(const float *__restrict__ q,
         for (int g = 0; g < D / 64; ++g) o[i][g] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const int kend = min(q0 + BM, t.len);
-    for (int k0 = 0; k0 < kend; k0 += BN) {
-        __syncthreads();
-        load_tile<BN, D>(Ks, kg, ldk, k0, t.len);
-        load_tile<BN, D>(Vs, vg, ldk, k0, t.len);
+    load_tile_async<BN, D>(KV, kg, ldk, 0, t.len);
+    load_tile_async<BN, D>(KV + TS, vg, ldk, 0, t.len);
+    async_commit();
+    for (int k0 = 0, b = 0; k0 < kend; k0 += BN, b ^= 1) {
+        const float *Ks = KV + 2 * b * TS, *Vs = Ks + TS;
+        if (k0 + BN < kend) {
+            float *next = KV + 2 * (b ^ 1) * TS;
+            load_tile_async<BN, D>(next, kg, ldk, k0 + BN, t.len);
+            load_tile_async<BN, D>(next + TS, vg, ldk, k0 + BN, t.len);
+        }
+        async_commit();
+        async_wait<1>();
         __syncthreads();
         float s[RPT][4] = {};
         mul_nt<RPT, D>(s, Qs, Ks, ra, tx);
@@ -203,6 +231,7 @@ __global__ void __launch_bounds__(NT) attn_fwd_simt(const float *__restrict__ q,
         }
         __syncwarp();  // a row's 16 threads lie in one warp
         mul_nn<RPT, D>(o, Ps, Vs, ra, tx);
+        __syncthreads();  // this block's tiles have been read
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
@@ -316,6 +345,7 @@ __global__ void __launch_bounds__(NT) attn_bwd_dq_simt(const float *__restrict__
     }
 }
 
+// dk and dv of one query head's (blockIdx.y) queries, laid out as [tokens, Hq, D].
 template <int D>
 __global__ void __launch_bounds__(NT) attn_bwd_dkv_simt(const float *__restrict__ q, const float *__restrict__ k,
                                                         const float *__restrict__ v, const float *__restrict__ dout,
@@ -330,7 +360,7 @@ __global__ void __launch_bounds__(NT) attn_bwd_dkv_simt(const float *__restrict_
           *dt = ls + 64;
     const AttnTile t = attn_tile(cu, B, Tn, 64, blockIdx.x);
     if (t.seq < 0) return;
-    const int hk = blockIdx.y, G = Hq / Hk;
+    const int h = blockIdx.y, hk = h / (Hq / Hk);
     const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
     // the tiles come last block first, the fewest queries: take them the other way round
     const int k0 = ((t.len + 63) / 64 - 1 - t.block) * 64;
@@ -338,30 +368,29 @@ __global__ void __launch_bounds__(NT) attn_bwd_dkv_simt(const float *__restrict_
     load_tile<64, D>(Ks, k + t.t0 * ldk + (int64_t)hk * D, ldk, k0, t.len);
     load_tile<64, D>(Vs, v + t.t0 * ldk + (int64_t)hk * D, ldk, k0, t.len);
     float4 ak[4][D / 64] = {}, av[4][D / 64] = {};
-    for (int h = hk * G; h < (hk + 1) * G; ++h)
-        for (int q0 = k0; q0 < t.len; q0 += 64) {
-            __syncthreads();
-            load_tile<64, D>(Qs, q + t.t0 * ldq + (int64_t)h * D, ldq, q0, t.len);
-            load_tile<64, D>(Os, dout + t.t0 * ldq + (int64_t)h * D, ldq, q0, t.len);
-            load_rowstats(ls, dt, lse, dot, t.t0, Hq, h, q0, t.len);
-            __syncthreads();
-            float p[4][4], ds[4][4];
-            tile_p_ds<D>(p, ds, Qs, Os, Ks, Vs, ls, dt, q0, k0, t.len, scale * kLog2e, ra, tx);
+    for (int q0 = k0; q0 < t.len; q0 += 64) {
+        __syncthreads();
+        load_tile<64, D>(Qs, q + t.t0 * ldq + (int64_t)h * D, ldq, q0, t.len);
+        load_tile<64, D>(Os, dout + t.t0 * ldq + (int64_t)h * D, ldq, q0, t.len);
+        load_rowstats(ls, dt, lse, dot, t.t0, Hq, h, q0, t.len);
+        __syncthreads();
+        float p[4][4], ds[4][4];
+        tile_p_ds<D>(p, ds, Qs, Os, Ks, Vs, ls, dt, q0, k0, t.len, scale * kLog2e, ra, tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    Ps[(ra + i) * LDP + tx + 16 * j] = p[i][j];
-                    Ds[(ra + i) * LDP + tx + 16 * j] = ds[i][j];
-                }
-            __syncthreads();
-            mul_tn<D>(av, Ps, Os, ra, tx);
-            mul_tn<D>(ak, Ds, Qs, ra, tx);
-        }
+            for (int j = 0; j < 4; ++j) {
+                Ps[(ra + i) * LDP + tx + 16 * j] = p[i][j];
+                Ds[(ra + i) * LDP + tx + 16 * j] = ds[i][j];
+            }
+        __syncthreads();
+        mul_tn<D>(av, Ps, Os, ra, tx);
+        mul_tn<D>(ak, Ds, Qs, ra, tx);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (k0 + ra + i >= t.len) continue;
-        const int64_t at = (t.t0 + k0 + ra + i) * ldk + (int64_t)hk * D;
+        const int64_t at = ((t.t0 + k0 + ra + i) * Hq + h) * D;
 #pragma unroll
         for (int g = 0; g < D / 64; ++g) {
             store4(dk + at + 4 * (tx + 16 * g),
@@ -369,6 +398,22 @@ __global__ void __launch_bounds__(NT) attn_bwd_dkv_simt(const float *__restrict_
             store4(dv + at + 4 * (tx + 16 * g), av[i][g]);
         }
     }
+}
+
+// dk and dv [tokens, Hk, D] from the G parts of each key head, added in order; a thread has 4 elements
+__global__ void __launch_bounds__(NT) attn_bwd_add_heads(const float *__restrict__ pk, const float *__restrict__ pv,
+                                                         float *__restrict__ dk, float *__restrict__ dv, int64_t n4, int G,
+                                                         int d4, const int32_t *__restrict__ cu, int B, int Hk)
+{
+    const int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x;
+    if (i >= (cu ? min(n4, (int64_t)max(cu[B], 0) * Hk * d4) : n4)) return;
+    const float4 *p = reinterpret_cast<const float4 *>(blockIdx.y ? pv : pk) + i / d4 * G * d4 + i % d4;
+    float4 x = p[0];
+    for (int g = 1; g < G; ++g) {
+        const float4 y = p[(int64_t)g * d4];
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    reinterpret_cast<float4 *>(blockIdx.y ? dv : dk)[i] = x;
 }
 
 template <int D, int RPT> cudaError_t run_fwd(const AttnArgs &a, cudaStream_t st)
@@ -398,16 +443,35 @@ template <int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t st)
     attn_bwd_dq_simt<D><<<dim3(tiles, a.Hq), NT, smem, st>>>((const float *)a.q, (const float *)a.k, (const float *)a.v,
                                                                 (const float *)a.dout, a.lse, dot, (float *)a.dq, a.cu, a.B,
                                                                 a.T, a.Hq, a.Hk, a.scale);
-    attn_bwd_dkv_simt<D><<<dim3(tiles, a.Hk), NT, smem, st>>>((const float *)a.q, (const float *)a.k, (const float *)a.v,
-                                                                 (const float *)a.dout, a.lse, dot, (float *)a.dk, (float *)a.dv,
-                                                                 a.cu, a.B, a.T, a.Hq, a.Hk, a.scale);
+    const bool shared = a.Hq > a.Hk;
+    float *pk = dot + (rows + 63) / 64 * 64, *pv = pk + rows * D;  // behind D, if heads are shared
+    attn_bwd_dkv_simt<D><<<dim3(tiles, a.Hq), NT, smem, st>>>(
+        (const float *)a.q, (const float *)a.k, (const float *)a.v, (const float *)a.dout, a.lse, dot,
+        shared ? pk : (float *)a.dk, shared ? pv : (float *)a.dv, a.cu, a.B, a.T, a.Hq, a.Hk, a.scale);
+    if (shared) {
+        const int64_t n4 = rows / a.Hq * a.Hk * (D / 4);
+        attn_bwd_add_heads<<<dim3((unsigned)((n4 + NT - 1) / NT), 2), NT, 0, st>>>(
+            pk, pv, (float *)a.dk, (float *)a.dv, n4, a.Hq / a.Hk, D / 4, a.cu, a.B, a.Hk);
+    }
     return cudaGetLastError();
 }
 
 }  // namespace
 
+size_t attn_bwd_simt_workspace(int B, int T, int Hq, int Hk, int d, int varlen)
+{
+    const size_t rows = (varlen ? (size_t)T : (size_t)B * T) * Hq, parts = Hq > Hk ? 2 * rows * d : 0;
+    return ((rows + 63) / 64 * 64 + parts) * sizeof(float);
+}
+
 cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t st)
 {
+    // Query rows a CTA: 64, but 32 or 16 where blocks of 64 would leave most SMs without one (256 tokens, 2
+    // heads, d 64: 22.8 us with 64, 16.7 with 32, 13.8 with 16; 512 tokens, 8 heads, d 128: 68, 52 and
+    // 74 us; 2 x 1024 tokens, 8 heads, d 64: 127, 139 and 196 us).
+    const long n = attn_tiles(a.cu, a.B, a.T, 64) * a.Hq;
+    if (n < 48) return a.d == 128 ? run_fwd<128, 1>(a, st) : run_fwd<64, 1>(a, st);
+    if (n < 148) return a.d == 128 ? run_fwd<128, 2>(a, st) : run_fwd<64, 2>(a, st);
     return a.d == 128 ? run_fwd<128, 4>(a, st) : run_fwd<64, 4>(a, st);
 }
 

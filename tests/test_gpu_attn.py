@@ -74,6 +74,35 @@ def test_packed(lengths, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B", [128, 129, 300])
+def test_packed_many_sequences(B, dtype):
+    lengths = np.random.RandomState(B).randint(0, 9, B)
+    lengths[[1, B // 2, B - 2]] = [200, 333, 129]
+    q, k, v, do = inputs((int(lengths.sum()) + 2,), 2, 1, 64, dtype, seed=B)
+    n = int(lengths.sum())
+    compare(q, k, v, do, dtype, cu=cu_of(lengths), rows=slice(0, n))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_training_calls_on_two_streams_at_once(dtype):
+    import linear_attention_sequence_rule_b200 as gdn
+    cases, alone = [], []
+    for i, (lead, Hq, Hk, d) in enumerate([((2, 700), 6, 2, 64), ((1, 1100), 4, 1, 128)]):
+        q, k, v, do = (x.cuda() for x in inputs(lead, Hq, Hk, d, dtype, seed=20 + i))
+        out, lse = gdn.attn_fwd(q, k, v)
+        cases.append((q, k, v, out, lse, do))
+        alone.append((out, lse, *gdn.attn_bwd(*cases[-1])))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cases], []
+    for _ in range(5):
+        for c, w, st in zip(cases, alone, streams):
+            got.append((w, (*gdn.attn_fwd(*c[:3], stream=st), *gdn.attn_bwd(*c, stream=st))))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for w, x in got for a, b in zip(w, x))
+    gdn.device_status()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_peaked_softmax_and_scale(dtype):
     # scores of +-60 and more: the running maximum moves far, most weights underflow
     q, k, v, do = inputs((1, 400), 2, 2, 128, dtype, seed=3, peak=6.0)

@@ -172,6 +172,53 @@ def test_append_leaves_rows_without_a_slot():
     append_both(x, x, slots, kc, ks, kc.copy(), ks.copy(), "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,page,Hk", [(64, 16, 2), (64, 32, 1), (128, 64, 1), (64, 128, 1), (128, 128, 2)])
+def test_append_many_rows(d, page, Hk, dtype):
+    """More than 2048 rows: runs of every length up to several pages, in any order, some behind held tokens."""
+    r = np.random.RandomState(page + d + 1)
+    added = np.concatenate([np.arange(0, 9), r.randint(1, 3 * page, 24), [5 * page + 3], np.ones(90, int)])
+    while added.sum() < 2200:
+        added = np.append(added, r.randint(1, 4 * page))
+    r.shuffle(added)
+    lens = r.randint(0, 2 * page, len(added))
+    width = max(pages_of(lens + added, page)) + 1
+    table, left = table_of(lens, page, width, seed=40, spare=sum(pages_of(added, page)) + len(added))
+    p = oa.plan(lens, added, table, left, 0, page, int(added.sum()) + 5)
+    P = int(max(p["table"].max(), left.max())) + 1
+    kc, ks = filled_cache(P, Hk, page, d, 41)
+    vc, vs = filled_cache(P, Hk, page, d, 42)
+    g = torch.Generator().manual_seed(43)
+    rows = len(p["slots"])
+    mag = torch.exp2(torch.randint(-6, 8, (rows, Hk, 1), generator=g).float())
+    x, y = ((torch.randn(rows, Hk, d, generator=g) * mag).to(DT[dtype]) for _ in range(2))
+    append_both(x, y, p["slots"], kc, ks, vc, vs, dtype)
+
+
+@pytest.mark.parametrize("rows", [40, 2400])
+def test_append_rows_out_of_order_on_a_page_are_not_written(rows):
+    """Behind a row without the next slot, and behind a slot given twice, a page's rows are left out."""
+    d, page, P = 64, 16, 160
+    slots = np.full(rows, -1)
+    slots[:9] = [3, 4, 4, 5, 6, 20, 22, 23, 40]
+    slots[20:25] = [64, 65, 66, 64, 65]
+    if rows > 100:
+        slots[62:67] = [100, 101, 102, 101, 102]  # across two blocks of rows
+        slots[2390:2396] = 130 + np.arange(6)
+    kept = slots.copy()
+    for i in (2, 3, 4, 6, 7, 23, 24, 65, 66):
+        if i < rows:
+            kept[i] = -1
+    kc, ks = filled_cache(P, 1, page, d, 44)
+    x = torch.randn(rows, 1, d, generator=torch.Generator().manual_seed(45)).bfloat16()
+    import linear_attention_sequence_rule_b200 as gdn
+    dev, sc = [torch.from_numpy(kc).cuda() for _ in range(2)], [torch.from_numpy(ks).float().cuda() for _ in range(2)]
+    gdn.cache_append(x.cuda(), x.cuda(), i32(slots), *dev, *sc)
+    wc, ws = oa.append(x, kept, kc, ks)
+    for c, s in zip(dev, sc):
+        assert np.array_equal(c.cpu().numpy(), wc) and np.array_equal(s.double().cpu().numpy(), ws)
+
+
 # ---- one-token attention ---------------------------------------------------------------------------
 
 def decode_both(q, kc, vc, ks, vs, table, lens, dtype, scale=None):
@@ -271,6 +318,105 @@ def test_decode_large_and_small_magnitudes(dtype):
     q = torch.randn(1, 4, d, generator=torch.Generator().manual_seed(30))
     q = q * torch.tensor([1e-3, 1.0, 30.0, 1e3]).view(1, 4, 1)
     decode_both(q.to(DT[dtype]), kc, vc, ks, vs, table, lens, dtype, scale=1e-4)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_decode_many_requests_some_long(page, dtype):
+    """Contexts that are not split and span more than 32 tiles a warp."""
+    import linear_attention_sequence_rule_b200 as gdn
+    d, n = 64, 1100
+    lens = np.random.RandomState(46).randint(0, 60, n)
+    lens[[3, 500, 1099]] = [4097, 9000, 8191]
+    width = 9100 // page
+    assert gdn.gdn_attn_decode_workspace_bytes(n, 2, 1, d, page, width, gdn._DT[DT[dtype]]) == 0
+    table, _ = table_of(lens, page, width, seed=47)
+    kc, ks = filled_cache(int(table.max()) + 1, 1, page, d, 48)
+    vc, vs = filled_cache(int(table.max()) + 1, 1, page, d, 49)
+    q = torch.randn(n, 2, d, generator=torch.Generator().manual_seed(50)).to(DT[dtype])
+    decode_both(q, kc, vc, ks, vs, table, lens, dtype, scale=0.02)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_heads_do_not_touch_one_another(dtype):
+    """A head's result does not depend on what the heads beside it hold: huge, tiny, infinite or NaN."""
+    import linear_attention_sequence_rule_b200 as gdn
+    lens, page, d = [100, 40], 32, 128
+    table, _ = table_of(lens, page, 4, seed=51)
+    P = int(table.max()) + 1
+    dev = [torch.from_numpy(filled_cache(P, 1, page, d, x)[0]).cuda() for x in (52, 53)]
+    sc = [torch.from_numpy(filled_cache(P, 1, page, d, x)[1]).float().cuda() for x in (52, 53)]
+    q = torch.randn(2, 12, d, generator=torch.Generator().manual_seed(54)).to(DT[dtype]).cuda()
+    f = lambda x: gdn.attn_decode(x, *dev, *sc, i32(table), i32(lens), scale=0.02)
+    want = f(q)
+    for h, bad in ((0, 2.0 ** 60), (5, 2.0 ** -60), (9, float("inf")), (11, float("nan"))):
+        y = q.clone()
+        y[:, h] *= bad
+        rest = [i for i in range(12) if i != h]
+        assert torch.equal(f(y)[:, rest], want[:, rest]), (h, bad)
+    gdn.device_status()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, give what each gives alone."""
+    import linear_attention_sequence_rule_b200 as gdn
+    page, d, n = 64, 128, 5
+    g = torch.Generator("cuda").manual_seed(55)
+    cases = []
+    for ctx in (3000, 700):
+        width = -(-ctx // page)
+        table = torch.randperm(n * width, generator=g, device="cuda").to(torch.int32).view(n, width)
+        cache = [torch.randint(0, 120, (n * width, 2, page, d), generator=g, device="cuda").to(torch.uint8) for _ in range(2)]
+        sc = [torch.full((n * width, 2), 2.0 ** -7, device="cuda") for _ in range(2)]
+        q = torch.randn(n, 8, d, generator=g, device="cuda").bfloat16()
+        cases.append((q, *cache, *sc, table, i32([ctx - 7 * i for i in range(n)])))
+    want = [gdn.attn_decode(*c, scale=0.01) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, st) in enumerate(zip(cases, streams)):
+            got[i].append(gdn.attn_decode(*c, scale=0.01, stream=st))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for xs, w in zip(got, want) for x in xs)
+    gdn.device_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nothing_is_written_outside_the_arrays(dtype):
+    """Outputs and workspaces that lie between marked bytes, at odd sizes."""
+    import linear_attention_sequence_rule_b200 as gdn
+    held = []
+
+    def guarded(*shape, dtype):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        raw = torch.full((n + 1024 + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+        at = 512 + (-(raw.data_ptr() + 512)) % 256
+        held.append((raw, at, n))
+        return raw[at:at + n].view(dtype).view(*shape)
+
+    dt, lengths, Hq, Hk, d, page = DT[dtype], [129, 1, 70, 0, 33], 6, 2, 64, 32
+    T, N, code = sum(lengths) + 3, len(lengths), gdn._DT[DT[dtype]]
+    g = torch.Generator().manual_seed(56)
+    q, do = (torch.randn(T, Hq, d, generator=g).to(dt).cuda() for _ in range(2))
+    k, v = (torch.randn(T, Hk, d, generator=g).to(dt).cuda() for _ in range(2))
+    table = guarded(N, 6, dtype=torch.int32).fill_(-1)
+    plan = gdn.cache_plan(i32([0] * N), i32(lengths), table, i32(range(20)), i32([0]), page, T,
+                          *(guarded(m, dtype=torch.int32) for m in (N + 1, T, T, N, 1, 2)))
+    assert plan.status.tolist() == [0, 0]
+    cache = [guarded(20, Hk, page, d, dtype=torch.uint8).zero_() for _ in range(2)]
+    sc = [guarded(20, Hk, dtype=torch.float32).zero_() for _ in range(2)]
+    gdn.cache_append(k, v, plan.slots, *cache, *sc)
+    out, lse = guarded(T, Hq, d, dtype=dt), guarded(T, Hq, dtype=torch.float32)
+    gdn.attn_fwd(q, k, v, cu_seqlens=plan.cu_seqlens, out=out, lse=lse)
+    grads = [guarded(T, h, d, dtype=dt) for h in (Hq, Hk, Hk)]
+    ws = guarded(gdn.gdn_attn_bwd_workspace_bytes(N, T, Hq, Hk, d, 1, code), dtype=torch.uint8)
+    gdn.attn_bwd(q, k, v, out, lse, do, plan.cu_seqlens, None, *grads, workspace=ws)
+    ws = guarded(gdn.gdn_attn_decode_workspace_bytes(N, Hq, Hk, d, page, 6, code), dtype=torch.uint8)
+    gdn.attn_decode(q[:N], *cache, *sc, table, plan.lens, out=guarded(N, Hq, d, dtype=dt), workspace=ws)
+    gdn.device_status()
+    for raw, at, n in held:
+        assert bool((raw[:at] == 0x5a).all()) and bool((raw[at + n:] == 0x5a).all())
 
 
 # ---- together --------------------------------------------------------------------------------------
