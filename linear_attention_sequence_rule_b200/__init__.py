@@ -901,14 +901,15 @@ def _run(fn, dev, stream, *args):
 
 
 def _new(stream, like, shape=None, dtype=None):
-    """A tensor taken for this call; the allocator keeps it until a stream that was given has passed."""
-    if shape is None:
-        t = torch.empty_like(like)
-    else:
-        t = like.new_empty(shape, dtype=dtype or like.dtype)
+    """A tensor taken for this call.  Memory for a stream that was given comes from that stream's own pool (what
+    the current stream freed, its pending kernels may still use), and the allocator does not hand it out
+    again before the current stream has passed."""
     if stream is not None:
-        t.record_stream(stream)
-    return t
+        with torch.cuda.stream(stream):
+            t = _new(None, like, shape, dtype)
+        t.record_stream(torch.cuda.current_stream(like.device))
+        return t
+    return torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype or like.dtype)
 
 
 @functools.lru_cache(maxsize=1024)

@@ -189,6 +189,22 @@ def test_repeats_bit_for_bit_on_another_stream_and_in_a_graph(dtype):
     gdn.device_status()
 
 
+def test_results_for_a_given_stream_take_no_memory_that_another_still_writes():
+    import linear_attention_sequence_rule_b200 as gdn
+    q, k, v, do = (x.cuda() for x in inputs((1, 300), 4, 4, 64, "bf16", seed=12))
+    out, lse = gdn.attn_fwd(q, k, v)
+    want = (out, lse, *gdn.attn_bwd(q, k, v, out, lse, do))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(int(2e7))  # the writes of memory that is free again are still to come
+    for x in want * 2:
+        torch.full_like(x, 7.0)
+    torch.empty(gdn.gdn_attn_bwd_workspace_bytes(1, 300, 4, 4, 64, 0, 0), dtype=torch.uint8, device="cuda").fill_(9)
+    got = (*gdn.attn_fwd(q, k, v, stream=side), *gdn.attn_bwd(q, k, v, out, lse, do, stream=side))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_gradients_are_the_forwards_differences():
     """fp32: the directional derivative from attn_bwd against a central difference of attn_fwd."""
     import linear_attention_sequence_rule_b200 as gdn
