@@ -448,7 +448,8 @@ GDN_API size_t gdn_attn_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d,
  *        length or more tokens than its table row holds}, {3, new tokens beyond rows, or 2^31 - 1},
  *        {4, 0}: free_head outside 0 .. num_free.  The first of 4, 2, 3, 1 that applies is given.
  * All int32.  1 <= N <= 16384, page in {16, 32, 64, 128}, max_blocks >= 1, max_blocks page < 2^31,
- * num_free >= 0, rows >= 0.  One launch, no workspace; arrays must not overlap but as named above.
+ * num_free >= 0, rows >= 0.  One launch, no workspace; arrays must not overlap but as named above;
+ * free_head, free_head_out and status need an alignment of 4 bytes only, the others of 16.
  */
 GDN_API int gdn_cache_plan(const int32_t *lens, const int32_t *added, int32_t *block_table,
                            const int32_t *free_list, const int32_t *free_head, int32_t *cu_seqlens,

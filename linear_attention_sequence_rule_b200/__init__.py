@@ -1030,12 +1030,17 @@ def cache_plan(lens, added, block_table, free_list, free_head, page, rows, cu_se
     _is(block_table, "block_table", i32, block_table.shape, dev)
     _is(free_list, "free_list", i32, free_list.shape, dev)
     _is(free_head, "free_head", i32, (1,), dev)
-    o = [cu_seqlens, slots, positions, lens_out, free_head_out, status]
-    if all(t is None for t in o):  # 16-byte aligned parts of one allocation
-        a, b, c = -(N + 1) & 3, -rows & 3, -N & 3
-        o = _new(stream, lens, (N + 1 + a + 2 * (rows + b) + N + c + 8,)).split_with_sizes(
-            (N + 1, a, rows, b, rows, b, N, c, 1, 3, 2, 2))[::2]
+    if (cu_seqlens is None and slots is None and positions is None and lens_out is None and free_head_out is None
+            and status is None):  # parts of one allocation; all but the last two 16-byte aligned
+        pads, sizes = (-rows & 3, -rows & 3, -N & 3), (rows, rows, N)
+        if any(pads):
+            sizes = (rows, pads[0], rows, pads[1], N, pads[2])
+        o = _new(stream, lens, (sum(sizes) + N + 4,)).split_with_sizes((*sizes, N + 1, 1, 2))
+        if any(pads):
+            o = (*o[:6:2], *o[6:])
+        o = (o[3], o[0], o[1], o[2], o[4], o[5])
     else:
+        o = [cu_seqlens, slots, positions, lens_out, free_head_out, status]
         names = ("cu_seqlens", "slots", "positions", "lens_out", "free_head_out", "status")
         for i, (t, n, name) in enumerate(zip(o, (N + 1, rows, rows, N, 1, 2), names)):
             if t is None:

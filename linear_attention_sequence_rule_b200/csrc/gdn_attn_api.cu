@@ -155,9 +155,11 @@ int gdn_cache_plan(const int32_t *lens, const int32_t *added, int32_t *block_tab
     if (!lens || !added || !block_table || !free_head || !cu_seqlens || !lens_out || !free_head_out || !status ||
         (num_free > 0 && !free_list) || (rows > 0 && (!slots || !positions)))
         return refuse(GDN_ERR_INVALID_ARGUMENT, "%s: every array is required", fn);
-    const void *ptrs[] = {lens, added, block_table, free_list, free_head, cu_seqlens, slots, positions, lens_out,
-                          free_head_out, status};
+    const void *ptrs[] = {lens, added, block_table, free_list, cu_seqlens, slots, positions, lens_out};
     if ((rc = check_pointers(fn, ptrs)) != GDN_OK) return rc;
+    for (const void *p : {(const void *)free_head, (const void *)free_head_out, (const void *)status})
+        if (reinterpret_cast<uintptr_t>(p) & 3u)
+            return refuse(GDN_ERR_INVALID_ARGUMENT, "%s: pointer %p is not 4-byte aligned", fn, p);
     const CachePlanArgs a{lens, added, block_table, free_list, free_head, cu_seqlens, slots, positions, lens_out,
                           free_head_out, status, N, max_blocks, num_free, rows, page};
     return launched(launch_cache_plan(a, static_cast<cudaStream_t>(stream)), fn);

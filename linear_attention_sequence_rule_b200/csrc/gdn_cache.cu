@@ -197,8 +197,9 @@ __global__ void __cluster_dims__(PC, 1, 1) __launch_bounds__(PT) cache_plan_kern
 //
 // Memory bounds it: 2 or 4 bytes in and 1 out an element.  A CTA takes a block of rows for one head, keys
 // or values, and finds the runs that begin there: short ones (a generation step's, of one row) go to
-// groups of lanes as wide as a row, side by side; the rows of a long one (a prompt's) are held in the CTA's
-// registers between the maximum and the quotients, so that they are read once.
+// groups of lanes as wide as a row, side by side; the rows of a long one (a prompt's) are held in registers
+// between the maximum and the quotients, so that they are read once, by as many warps as four loads a lane
+// take for a page, so that a CTA has several runs of small pages under way.
 
 constexpr int AT = 256;  // threads per CTA
 
@@ -319,8 +320,20 @@ __device__ __forceinline__ void append_run(const T *x, int64_t ld, uint8_t *base
     if (c == 0) *scale = to;
 }
 
-// Loads of 16 bytes a thread that hold a page's rows of one head in a CTA's registers.
-template <typename T, int D, int PAGE> constexpr int NPB = (PAGE * (D / Vec16<T>::N) + AT - 1) / AT;
+// Threads that hold a page's rows of one head, with four loads of 16 bytes each (the whole CTA with up to 16), and
+// the loads.  (Prompts of 32768 rows of 4 heads, bf16, 128 rows a CTA: pages of 16, d 64: 21 us, and 34 by the CTA with
+// one load a thread; d 128: 35 us with four, and 39 with eight, which leave room for 3 CTAs an SM instead of 5.)
+template <typename T, int D, int PAGE>
+constexpr int HOLD = PAGE * (D / Vec16<T>::N) / 4 < AT ? PAGE * (D / Vec16<T>::N) / 4 : AT;
+template <typename T, int D, int PAGE> constexpr int NPB = PAGE * (D / Vec16<T>::N) / HOLD<T, D, PAGE>;
+
+// A barrier of the N threads of group `g` of the CTA.
+template <int N> __device__ __forceinline__ void group_sync(int g)
+{
+    if (N == 32) __syncwarp();
+    else if (N == AT) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(N) : "memory");
+}
 
 template <typename T, int D, int PAGE, int TILE>
 __global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append_kernel(const T *__restrict__ k, const T *__restrict__ v,
@@ -330,6 +343,8 @@ __global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append
 {
     constexpr int E = Vec16<T>::N, C = D / E, RP = AT / C;  // threads a row, rows at a time
     constexpr int NP = NPB<T, D, PAGE>;                     // registers: NP x 16 bytes
+    constexpr int GT = HOLD<T, D, PAGE>, GW = GT / 32;      // threads and warps that share a long run
+    static_assert(GT >= 32 && AT % GT == 0, "whole warps");
     __shared__ float s_max[AT / 32];
     constexpr int kShortRun = 4;                            // up to this length a run goes to a group of lanes
     constexpr int SPAN = (TILE + PAGE + 31) & ~31;          // rows looked at
@@ -381,37 +396,45 @@ __global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append
                          slot & (PAGE - 1), c, group);
     }
     if (!__syncthreads_or(tid < TILE && leads(tid) && length(tid) > kShortRun)) return;
+    // group `grp` takes every (AT / GT)-th long run; this thread has a part of its rows r0, r0 + RH, ...
+    constexpr int RH = GT / C;
+    const int grp = tid / GT, r0 = tid % GT / C;
+    int turn = 0;
     for (int q = 0; q < (TILE + 31) / 32; ++q)
         for (uint32_t left = s_lead[q]; left; left &= left - 1) {
             const int at = 32 * q + __ffs(left) - 1, t = tile0 + at, n = length(at);
             if (n <= kShortRun) continue;
+            if (GT < AT && (turn++ & (AT / GT - 1)) != grp) continue;
             const int slot = s_slot[at], pg = slot >> shift, off = slot & (PAGE - 1);
             const T *xr = x + (int64_t)t * ld;
             Vec16<T> y[NP];
             float mx = 0.f;
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                if (rr + RP * i < n) y[i].load(xr + (int64_t)(rr + RP * i) * ld);
+                if (r0 + RH * i < n) y[i].load(xr + (int64_t)(r0 + RH * i) * ld);
             const int64_t ph = (int64_t)pg * Hk + h;
             const float was = off ? scale[ph] : 0.f;
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                if (rr + RP * i < n) mx = y[i].amax(mx);
+                if (r0 + RH * i < n) mx = y[i].amax(mx);
 #pragma unroll
             for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane == 0) s_max[tid >> 5] = mx;
-            __syncthreads();
-            mx = s_max[0];
+            if (GW > 1) {
+                if (lane == 0) s_max[tid >> 5] = mx;
+                group_sync<GT>(grp);
+                mx = s_max[grp * GW];
 #pragma unroll
-            for (int i = 1; i < AT / 32; ++i) mx = fmaxf(mx, s_max[i]);
+                for (int i = 1; i < GW; ++i) mx = fmaxf(mx, s_max[grp * GW + i]);
+            }
             const float to = fmaxf(was, scale_of(mx)), inv = 1.f / to;
             uint8_t *base = cache + (ph << shift) * D + E * c;
-            if (off && to != was) shrink_rows<D, E, RP>(base, rr, off, was * inv);
+            if (off && to != was) shrink_rows<D, E, RH>(base, r0, off, was * inv);
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                if (rr + RP * i < n) y[i].store(base + (off + rr + RP * i) * D, inv);
-            __syncthreads();  // s_max is read, and every thread has the old scale
-            if (tid == 0) scale[ph] = to;
+                if (r0 + RH * i < n) y[i].store(base + (off + r0 + RH * i) * D, inv);
+            // s_max is read, and every thread has the old scale
+            group_sync<GT>(grp);
+            if (tid % GT == 0) scale[ph] = to;
         }
 }
 
@@ -419,9 +442,11 @@ template <typename T, int D, int PAGE> cudaError_t run_append(const CacheAppendA
 {
     // Rows a CTA: few where rows are few, so that a generation step's spread over the SMs (256 rows of 4 heads,
     // d 128, page 64, bf16: 2.5 us with 16, 5.3 with 64), more where they are many (prompts of 32768 rows, d 64:
-    // 30 us with 16, 19 with 64, for 7.8 at the copy rate).
-    const int tile = a.rows <= 2048 ? 16 : 64;
-    auto kern = tile == 16 ? cache_append_kernel<T, D, PAGE, 16> : cache_append_kernel<T, D, PAGE, 64>;
+    // 30 us with 16, 22 with 64, 17 with 128, for 7.8 at the copy rate), but 64 where they all fit the SMs at once
+    // (4096 rows, d 64: 4.3 us with 64, 4.7 with 128; d 128: 5.0 and 6.0).
+    const int tile = a.rows <= 2048 ? 16 : (long)a.rows / 64 * a.Hk * 2 <= 5 * 148 ? 64 : 128;
+    auto kern = tile == 16 ? cache_append_kernel<T, D, PAGE, 16> : tile == 64 ? cache_append_kernel<T, D, PAGE, 64>
+                                                                             : cache_append_kernel<T, D, PAGE, 128>;
     kern<<<dim3((a.rows + tile - 1) / tile, a.Hk, 2), AT, 0, st>>>((const T *)a.k, (const T *)a.v, a.slots, a.k_cache,
                                                                    a.v_cache, a.k_scale, a.v_scale, a.rows, a.Hk,
                                                                    a.num_pages);

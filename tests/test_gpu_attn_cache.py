@@ -103,6 +103,9 @@ def test_plan_in_place_and_empty():
     for _ in range(40):  # lens and free_head updated in place, one token a step
         p = gdn.cache_plan(lens, i32([1, 0, 0]), t, i32(left), head, 16, 4, lens_out=lens, free_head_out=head)
     assert lens.tolist() == [43, 16, 0] and head.tolist() == [2] and p.positions.tolist() == [42, -1, -1, -1]
+    few = i32([7, 0, 9, 8, 7])  # the single numbers may lie anywhere
+    p = gdn.cache_plan(lens, i32([0, 0, 0]), t, i32(left), few[1:2], 16, 0, free_head_out=few[1:2], status=few[2:4])
+    assert few.tolist() == [7, 0, 0, 0, 7]
     p = gdn.cache_plan(lens, i32([0, 0, 0]), t, i32([]), i32([0]), 16, 0)
     assert p.status.tolist() == [0, 0] and p.slots.numel() == 0 and p.cu_seqlens.tolist() == [0] * 4
 
@@ -173,7 +176,8 @@ def test_append_leaves_rows_without_a_slot():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("d,page,Hk", [(64, 16, 2), (64, 32, 1), (128, 64, 1), (64, 128, 1), (128, 128, 2)])
+@pytest.mark.parametrize("d,page,Hk", [(64, 16, 2), (64, 32, 1), (128, 64, 1), (64, 128, 1), (128, 128, 2), (128, 16, 12),
+                                       (128, 32, 12), (64, 16, 12), (64, 64, 12), (128, 64, 12)])
 def test_append_many_rows(d, page, Hk, dtype):
     """More than 2048 rows: runs of every length up to several pages, in any order, some behind held tokens."""
     r = np.random.RandomState(page + d + 1)
