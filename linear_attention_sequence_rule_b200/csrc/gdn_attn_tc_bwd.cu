@@ -50,6 +50,29 @@ constexpr int HT = 64;           // rows of the other side a step
 constexpr int kHalf = HT * 128;  // bytes from a tile's first half to its second (in each sub-tile)
 constexpr int kExactBlocks = 2;
 
+// N tiles in tensor memory that the steps take in turn, step i tile i % N.  Even and odd steps belong to
+// different warps, and a warp that passes over phases of a barrier cannot tell them by parity: so each barrier
+// belongs to steps of one parity, and with three tiles there are six.
+template <int N> struct Turns {
+    static constexpr int TILES = N, BARS = N % 2 ? 2 * N : N;
+    __device__ __forceinline__ static int tile(int i) { return i % N; }
+    __device__ __forceinline__ static int bar(int i) { return i % BARS; }
+    __device__ __forceinline__ static int phase(int i) { return i / BARS; }
+    // the same for the steps of one parity, counted up
+    int b, ph = 0;
+    __device__ __forceinline__ explicit Turns(int first) : b(first) {}
+    __device__ __forceinline__ int tile() const { return N == 2 ? b : b >= N ? b - N : b; }
+    __device__ __forceinline__ void next()
+    {
+        if (N == 2) {
+            ++ph;
+        } else if ((b += 2) >= BARS) {
+            b -= BARS;
+            ++ph;
+        }
+    }
+};
+
 // D[128 x D] (+)= A B over a step's 64 rows of B: A (bf16) in two chunks of 32 columns (16 of tensor
 // memory) that lie 32 apart
 template <int D>
@@ -79,6 +102,9 @@ __device__ __forceinline__ void drain_loads(uint64_t *bar, int first, int count)
 // load would be waited for.
 template <int D> struct DqCfg {
     static constexpr int NK = D == 64 ? 4 : 3, NV = D == 64 ? 4 : 2;
+    using TS = Turns<D == 64 ? 3 : 2>;  // tiles of S
+    using TP = Turns<D == 64 ? 3 : 2>;  // tiles of dP
+    static constexpr bool BOTH = TS::TILES == 3;  // both tiles of a step are there when it begins
     static constexpr int TILE = BT * D * 2;
     static constexpr int Q = 0, O = TILE, K = 2 * TILE, V = K + NK * TILE, RED = V + NV * TILE, BAR = RED + 2 * BT * 4;
     static constexpr int q_full = 0;               // Q and dO
@@ -88,19 +114,19 @@ template <int D> struct DqCfg {
     static constexpr int v_empty = k_empty + NK;   // [NV]
     static constexpr int k_zeroed = v_empty + NV;  // [NK] the stage has no row behind the end (ragged ends only)
     static constexpr int v_zeroed = k_zeroed + NK; // [NV]
-    static constexpr int s_full = v_zeroed + NV;   // [2]
-    static constexpr int dp_full = s_full + 2;     // [2]
-    static constexpr int s_free = dp_full + 2;     // [2] S has been read
-    static constexpr int ds_full = s_free + 2;     // [2] dS is there (first pass: dP has been read)
-    static constexpr int dq_done = ds_full + 2;    // [2] dS has been used
-    static constexpr int a_full = dq_done + 2;     // Q and dO are in tensor memory
+    static constexpr int s_full = v_zeroed + NV;        // [TS] one a turn: S (BOTH: S and dP)
+    static constexpr int dp_full = s_full + TS::BARS;   // [TP] dP
+    static constexpr int s_free = dp_full + TP::BARS;   // [TS] S has been read
+    static constexpr int ds_full = s_free + TS::BARS;   // [TP] dS is there (first pass: dP has been read)
+    static constexpr int dq_done = ds_full + TP::BARS;  // [TP] dS has been used
+    static constexpr int a_full = dq_done + TP::BARS;   // Q and dO are in tensor memory
     static constexpr int all_done = a_full + 1;    // dQ is there (a barrier of one phase: a warp that
                                                    // passes over phases cannot tell them by parity)
     static constexpr int drain = all_done + 1;     // [3]
     static constexpr int NBAR = drain + 3;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
-    static constexpr uint32_t tS = 0, tP = 128, tG = 256, tQ = 256 + D, tO = tQ + D / 2;  // S[2], dP[2], dQ, Q, dO
+    static constexpr uint32_t tS = 0, tP = HT * TS::TILES, tG = tP + HT * TP::TILES, tQ = tG + D, tO = tQ + D / 2;
     static_assert(tO + D / 2 <= 512, "tensor memory budget");
     static_assert(TOTAL <= 232448, "shared memory budget");
 };
@@ -114,6 +140,8 @@ __global__ void __launch_bounds__(NTH, 1)
                    int Hq, int Hk, float scale, int64_t tokens)
 {
     using C = DqCfg<D>;
+    using TS = typename C::TS;
+    using TP = typename C::TP;
     constexpr int NK = C::NK, NV = C::NV;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -136,7 +164,8 @@ __global__ void __launch_bounds__(NTH, 1)
 
     if (tid == 0) {
         for (int i = 0; i < C::NBAR; ++i)
-            mbar_init(&bar[i], i == C::a_full ? NEL / 32 : i >= C::s_free && i < C::dq_done ? NEL / 64 : 1);  // one a warp
+            mbar_init(&bar[i], i == C::a_full ? NEL / 32 : i >= C::s_free && i < C::dq_done ? NEL / 64  // one a warp
+                               : C::BOTH && i >= C::s_full && i < C::dp_full ? 2 : 1);
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -197,10 +226,10 @@ __global__ void __launch_bounds__(NTH, 1)
                         w.wait(&bar[C::k_full + j % NK], j / NK);
                         if (rows < BT) w.wait(&bar[C::k_zeroed + j % NK], j / NK);
                     }
-                    if (i > 1) w.wait(&bar[C::s_free + (i & 1)], (i >> 1) - 1);
+                    if (i >= TS::TILES) w.wait(&bar[(C::BOTH ? C::ds_full : C::s_free) + TS::bar(i - TS::TILES)], TS::phase(i - TS::TILES));
                     tc_fence_after();
-                    mma_nt_ta<D, HT>(tmem + C::tS + HT * (i & 1), tmem + C::tQ, sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf);
-                    commit(&bar[C::s_full + (i & 1)]);
+                    mma_nt_ta<D, HT>(tmem + C::tS + HT * TS::tile(i), tmem + C::tQ, sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf);
+                    commit(&bar[C::s_full + TS::bar(i)]);
                 }
         } else if (warp == 17) {  // dP
             w.wait(&bar[C::a_full], 0);
@@ -211,22 +240,22 @@ __global__ void __launch_bounds__(NTH, 1)
                         w.wait(&bar[C::v_full + j % NV], j / NV);
                         if (rows < BT) w.wait(&bar[C::v_zeroed + j % NV], j / NV);
                     }
-                    if (i > 1) w.wait(&bar[C::dq_done + (i & 1)], (i >> 1) - 1);
+                    if (i >= TP::TILES) w.wait(&bar[C::dq_done + TP::bar(i - TP::TILES)], TP::phase(i - TP::TILES));
                     tc_fence_after();
-                    mma_nt_ta<D, HT>(tmem + C::tP + HT * (i & 1), tmem + C::tO, sm + C::V + (j % NV) * C::TILE + (s & 1) * kHalf);
-                    commit(&bar[C::dp_full + (i & 1)]);
+                    mma_nt_ta<D, HT>(tmem + C::tP + HT * TP::tile(i), tmem + C::tO, sm + C::V + (j % NV) * C::TILE + (s & 1) * kHalf);
+                    commit(&bar[(C::BOTH ? C::s_full : C::dp_full) + TP::bar(i)]);
                     if ((s & 1) || s == n - 1) commit(&bar[C::v_empty + j % NV]);
                 }
         } else {  // dQ
             for (int p = 0, i = 0; p < passes; ++p)
                 for (int s = 0; s < n && !w.stopped(); ++s, ++i) {
                     const int j = p * nt + (s >> 1);
-                    w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
+                    w.wait(&bar[C::ds_full + TP::bar(i)], TP::phase(i));
                     tc_fence_after();
                     if (p == passes - 1)
-                        mma_step<D>(tmem + C::tG, tmem + C::tP + HT * (i & 1),
+                        mma_step<D>(tmem + C::tG, tmem + C::tP + HT * TP::tile(i),
                                     sm + C::K + (j % NK) * C::TILE + (s & 1) * kHalf, s > 0);
-                    commit(&bar[C::dq_done + (i & 1)]);
+                    commit(&bar[C::dq_done + TP::bar(i)]);
                     if ((s & 1) || s == n - 1) commit(&bar[C::k_empty + j % NK]);
                 }
             commit(&bar[C::all_done]);
@@ -279,22 +308,27 @@ __global__ void __launch_bounds__(NTH, 1)
         bool joined = !exact;
         if (joined) join();
         const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e), nl2 = pack2(nl, nl);
-        const uint32_t tS = tmem + lanes + C::tS + HT * set + c0, tP = tmem + lanes + C::tP + HT * set + c0;
-        for (int i = set; i < steps; i += 2) {
+        TS ts(set);
+        TP tp(set);
+        for (int i = set; i < steps; i += 2, ts.next(), tp.next()) {
             if (!joined && i >= n) {
                 join();
                 joined = true;
             }
             const uint64_t nd2 = pack2(nd, nd);
-            const int key0 = (i % n) * HT + c0 - at.block * BT;  // of this thread's columns, as r counts
-            float s[32];
-            w.wait(&bar[C::s_full + (i & 1)], i >> 1);
-            if (w.stopped()) break;
+            const int key0 = (i < n ? i : i - n) * HT + c0 - at.block * BT;  // of this thread's columns, as r counts
+            const uint32_t tS = tmem + lanes + C::tS + HT * ts.tile() + c0, tP = tmem + lanes + C::tP + HT * tp.tile() + c0;
+            float s[32], dp[32];
+            w.wait(&bar[C::s_full + ts.b], ts.ph);
+            __syncwarp();
             tc_fence_after();
             tmem_ld32(tS, s);
+            if (C::BOTH) tmem_ld32(tP, dp);
             tmem_wait_ld();
-            tc_fence_before();
-            warp_arrive(&bar[C::s_free + (i & 1)], lane);
+            if (!C::BOTH) {
+                tc_fence_before();
+                warp_arrive(&bar[C::s_free + ts.b], lane);
+            }
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
                 unpack2(fma2(pack2(s[x], s[x + 1]), sc2, nl2), s[x], s[x + 1]);
@@ -306,11 +340,12 @@ __global__ void __launch_bounds__(NTH, 1)
                 for (int x = 0; x < 32; ++x)
                     if (key0 + x > r) s[x] = 0.f;
             }
-            float dp[32];
-            w.wait(&bar[C::dp_full + (i & 1)], i >> 1);
-            tc_fence_after();
-            tmem_ld32(tP, dp);
-            tmem_wait_ld();
+            if (!C::BOTH) {
+                w.wait(&bar[C::dp_full + tp.b], tp.ph);
+                tc_fence_after();
+                tmem_ld32(tP, dp);
+                tmem_wait_ld();
+            }
             if (exact && i < n) {
                 uint64_t acc = 0;
 #pragma unroll
@@ -330,7 +365,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 tmem_wait_st();
             }
             tc_fence_before();
-            warp_arrive(&bar[C::ds_full + (i & 1)], lane);
+            warp_arrive(&bar[C::ds_full + tp.b], lane);
         }
         if (!joined) join();  // no step in the second pass, or left early: the other warps still come by
         if (!w.stopped()) {
@@ -354,6 +389,8 @@ __global__ void __launch_bounds__(NTH, 1)
 
 template <int D> struct DkvCfg {
     static constexpr int NS = D == 64 ? 4 : 2;
+    using TS = Turns<D == 64 ? 3 : 2>;  // tiles of S^T
+    using TP = Turns<D == 64 ? 3 : 2>;  // tiles of dP^T
     static constexpr int TILE = BT * D * 2;
     static constexpr int K = 0, V = TILE, Q = 2 * TILE, O = Q + NS * TILE, ST = O + NS * TILE, BAR = ST + NS * 2 * BT * 4;
     static constexpr int kv_full = 0;
@@ -361,21 +398,20 @@ template <int D> struct DkvCfg {
     static constexpr int o_full = q_full + NS;     // [NS] dO
     static constexpr int empty = o_full + NS;      // [NS] dV and dK have used the stage
     static constexpr int zeroed = empty + NS;      // [NS] the stage has no row behind the end (ragged ends only)
-    static constexpr int s_full = zeroed + NS;     // [2]
-    static constexpr int dp_full = s_full + 2;     // [2]
-    static constexpr int p_full = dp_full + 2;     // [2] P^T is there
-    static constexpr int ds_full = p_full + 2;     // [2] dS^T is there
-    static constexpr int dv_done = ds_full + 2;    // [2] P^T has been used
-    static constexpr int dk_done = dv_done + 2;    // [2] dS^T has been used
-    static constexpr int a_full = dk_done + 2;     // K (and V) are in tensor memory
+    static constexpr int s_full = zeroed + NS;          // [TS] one a turn:
+    static constexpr int dp_full = s_full + TS::BARS;   // [TP]
+    static constexpr int p_full = dp_full + TP::BARS;   // [TS] P^T is there
+    static constexpr int ds_full = p_full + TS::BARS;   // [TP] dS^T is there
+    static constexpr int dv_done = ds_full + TP::BARS;  // [TS] P^T has been used
+    static constexpr int dk_done = dv_done + TS::BARS;  // [TP] dS^T has been used
+    static constexpr int a_full = dk_done + TP::BARS;   // K (and V) are in tensor memory
     static constexpr int all_done = a_full + 1;    // dV and dK are there
     static constexpr int drain = all_done + 1;     // [4]
     static constexpr int NBAR = drain + 4;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
-    static constexpr bool TA = D == 64;            // K and V in tensor memory
-    // S^T[2], dP^T[2], dV, dK, (K, V)
-    static constexpr uint32_t tS = 0, tP = 128, tGV = 256, tGK = tGV + D, tK = tGK + D, tV = tK + D / 2;
+    static constexpr bool TA = false;            // K and V in tensor memory
+    static constexpr uint32_t tS = 0, tP = HT * TS::TILES, tGV = tP + HT * TP::TILES, tGK = tGV + D, tK = tGK + D, tV = tK + D / 2;
     static_assert(TA ? tV + D / 2 <= 512 : tK <= 512, "tensor memory budget");
 };
 
@@ -388,6 +424,8 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
                     float scale, int64_t tokens)
 {
     using C = DkvCfg<D>;
+    using TS = typename C::TS;
+    using TP = typename C::TP;
     constexpr int NS = C::NS;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -476,34 +514,34 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
-                    if (i > 1) w.wait(&bar[C::dv_done + (i & 1)], (i >> 1) - 1);
+                    if (i >= TS::TILES) w.wait(&bar[C::dv_done + TS::bar(i - TS::TILES)], TS::phase(i - TS::TILES));
                     if (!(x & 1)) {
                         w.wait(&bar[C::q_full + s], j / NS);
                         if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     }
                     tc_fence_after();
                     if (C::TA)
-                        mma_nt_ta<D, HT>(tmem + C::tS + HT * (i & 1), tmem + C::tK, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
+                        mma_nt_ta<D, HT>(tmem + C::tS + HT * TS::tile(i), tmem + C::tK, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
                     else
-                        mma_nt<D, HT>(tmem + C::tS + HT * (i & 1), sm + C::K, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
-                    commit(&bar[C::s_full + (i & 1)]);
+                        mma_nt<D, HT>(tmem + C::tS + HT * TS::tile(i), sm + C::K, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
+                    commit(&bar[C::s_full + TS::bar(i)]);
                 }
         } else if (warp == 17) {  // dP^T
             w.wait(&bar[C::TA ? C::a_full : C::kv_full], 0);
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
-                    if (i > 1) w.wait(&bar[C::dk_done + (i & 1)], (i >> 1) - 1);
+                    if (i >= TP::TILES) w.wait(&bar[C::dk_done + TP::bar(i - TP::TILES)], TP::phase(i - TP::TILES));
                     if (!(x & 1)) {
                         w.wait(&bar[C::o_full + s], j / NS);
                         if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     }
                     tc_fence_after();
                     if (C::TA)
-                        mma_nt_ta<D, HT>(tmem + C::tP + HT * (i & 1), tmem + C::tV, sm + C::O + s * C::TILE + (x & 1) * kHalf);
+                        mma_nt_ta<D, HT>(tmem + C::tP + HT * TP::tile(i), tmem + C::tV, sm + C::O + s * C::TILE + (x & 1) * kHalf);
                     else
-                        mma_nt<D, HT>(tmem + C::tP + HT * (i & 1), sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
-                    commit(&bar[C::dp_full + (i & 1)]);
+                        mma_nt<D, HT>(tmem + C::tP + HT * TP::tile(i), sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
+                    commit(&bar[C::dp_full + TP::bar(i)]);
                 }
         } else if (warp == 18) {  // dV
             for (int g = 0, i = 0; g < G; ++g)
@@ -513,10 +551,10 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
                         w.wait(&bar[C::o_full + s], j / NS);
                         if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     }
-                    w.wait(&bar[C::p_full + (i & 1)], i >> 1);
+                    w.wait(&bar[C::p_full + TS::bar(i)], TS::phase(i));
                     tc_fence_after();
-                    mma_step<D>(tmem + C::tGV, tmem + C::tS + HT * (i & 1), sm + C::O + s * C::TILE + (x & 1) * kHalf, i > 0);
-                    commit(&bar[C::dv_done + (i & 1)]);
+                    mma_step<D>(tmem + C::tGV, tmem + C::tS + HT * TS::tile(i), sm + C::O + s * C::TILE + (x & 1) * kHalf, i > 0);
+                    commit(&bar[C::dv_done + TS::bar(i)]);
                     if ((x & 1) || x == n - 1) commit(&bar[C::empty + s]);
                 }
             commit(&bar[C::all_done]);
@@ -524,10 +562,10 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int s = (g * nt + (x >> 1)) % NS;
-                    w.wait(&bar[C::ds_full + (i & 1)], i >> 1);
+                    w.wait(&bar[C::ds_full + TP::bar(i)], TP::phase(i));
                     tc_fence_after();
-                    mma_step<D>(tmem + C::tGK, tmem + C::tP + HT * (i & 1), sm + C::Q + s * C::TILE + (x & 1) * kHalf, i > 0);
-                    commit(&bar[C::dk_done + (i & 1)]);
+                    mma_step<D>(tmem + C::tGK, tmem + C::tP + HT * TP::tile(i), sm + C::Q + s * C::TILE + (x & 1) * kHalf, i > 0);
+                    commit(&bar[C::dk_done + TP::bar(i)]);
                     if ((x & 1) || x == n - 1) commit(&bar[C::empty + s]);
                 }
             commit(&bar[C::all_done]);
@@ -541,7 +579,6 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
         const int g = warp >> 2, wq = warp & 3, r = tid & (BT - 1);  // r: key row
         const int set = g >> 1, c0 = 32 * (g & 1);  // steps of this parity, these columns
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
-        const uint32_t tS = tmem + lanes + C::tS + HT * set + c0, tP = tmem + lanes + C::tP + HT * set + c0;
         const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e);
         if (C::TA) {  // groups 0, 1: halves of K's rows, 2, 3: of V's
             w.wait(&bar[C::kv_full], 0);
@@ -550,13 +587,18 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             tc_fence_before();
             warp_arrive(&bar[C::a_full], lane);
         }
-        for (int i = set; i < steps; i += 2) {
-            const int x0 = i % n, j = i / n * nt + (x0 >> 1), s = j % NS;
+        TS ts(set);
+        TP tp(set);
+        int x0 = set, j0 = 0;  // step of a head's, and the head's first tile
+        for (int i = set; i < steps; i += 2, x0 += 2, ts.next(), tp.next()) {
+            for (; x0 >= n; x0 -= n) j0 += nt;
+            const int j = j0 + (x0 >> 1), s = j % NS;
             const float *st = reinterpret_cast<const float *>(sm + C::ST) + s * 2 * BT + (x0 & 1) * HT + c0;
-            float p[32];
-            w.wait(&bar[C::s_full + (i & 1)], i >> 1);
+            const uint32_t tS = tmem + lanes + C::tS + HT * ts.tile() + c0, tP = tmem + lanes + C::tP + HT * tp.tile() + c0;
+            float p[32], dp[32];
+            w.wait(&bar[C::s_full + ts.b], ts.ph);
             w.wait(&bar[C::q_full + s], j / NS);  // over by now: for the rows' -lse and -D
-            if (w.stopped()) break;
+            __syncwarp();
             tc_fence_after();
             tmem_ld32(tS, p);
             tmem_wait_ld();
@@ -582,10 +624,9 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&bar[C::p_full + (i & 1)], lane);
-            w.wait(&bar[C::dp_full + (i & 1)], i >> 1);
+            warp_arrive(&bar[C::p_full + ts.b], lane);
+            w.wait(&bar[C::dp_full + tp.b], tp.ph);
             tc_fence_after();
-            float dp[32];
             tmem_ld32(tP, dp);
             tmem_wait_ld();
             uint32_t ds[16];
@@ -601,7 +642,7 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             tmem_st16(tP, ds);
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&bar[C::ds_full + (i & 1)], lane);
+            warp_arrive(&bar[C::ds_full + tp.b], lane);
         }
         if (!w.stopped()) {
             w.wait(&bar[C::all_done], 0);
