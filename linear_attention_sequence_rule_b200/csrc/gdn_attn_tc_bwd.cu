@@ -17,13 +17,17 @@
 // the key side, head by head ([Hq][tokens] each), into the workspace.
 //
 // Both kernels work in steps of 64 keys (query side) or 64 queries (key side): 128 x 64 tiles of S and
-// dP, two of each in tensor memory beside the gradients (2 x 64 + 2 x 64 + 256 columns at d = 128), so
-// that the products of one step run while the other's elements are worked on.  Steps of 128 with one
-// dP (or, on the key side, one S) buffer spend half their time in the chain of waits between products
-// and elements (about 1900 cycles a step with products and exponentials taken out); a product 64 wide
-// of two shared operands takes 48 cycles for 32 cycles' work, so the operands that stay for the whole CTA
-// are moved to tensor memory: Q and dO on the query side, K and V on the key side at d = 64 (at d = 128 there
-// is no room for them; with K there and one dP tile a step takes 1920 cycles, with two dP tiles 1640).
+// dP in tensor memory beside the gradients, two of each at d = 128 (2 x 64 + 2 x 64 + 256 columns) and three at
+// d = 64, so that the products of the next steps run while a step's elements are worked on.  What bounds them is
+// the chain of waits between products and elements: at d = 64 a query-side step takes 900 cycles, of which 512
+// are its exponentials; without products and element-wise work it still takes 540.  Steps of 128 with one dP (or,
+// on the key side, one S) tile spend 1900 cycles each on it, and half again as many element-wise warps
+// change nothing.
+// A product 64 wide of two shared operands takes 48 cycles for 32 cycles' work, so the query side moves Q and dO
+// to tensor memory.  The key side leaves K and V in shared memory: at d = 64 a third tile of S and dP gives more
+// (8 x 4096 tokens, 12 heads on 4: 412 us, with K and V in their place 455), at d = 128 there is no room (with K
+// there and one dP tile a step takes 1920 cycles, with two dP tiles 1640).
+// 16384 tokens, 16 heads on 4: query side 1.19 ms at d = 128 and 0.88 at d = 64, key side 1.69 and 1.02 ms.
 //   warps 0-7, 8-15  element by element, the even and the odd steps: a thread has a row, 32 columns
 //   warps 16-18      issue the products (key side: 16-19; one product a warp, since its waits and commits
 //                    take longer than the product)
@@ -404,15 +408,14 @@ template <int D> struct DkvCfg {
     static constexpr int ds_full = p_full + TS::BARS;   // [TP] dS^T is there
     static constexpr int dv_done = ds_full + TP::BARS;  // [TS] P^T has been used
     static constexpr int dk_done = dv_done + TS::BARS;  // [TP] dS^T has been used
-    static constexpr int a_full = dk_done + TP::BARS;   // K (and V) are in tensor memory
-    static constexpr int all_done = a_full + 1;    // dV and dK are there
+    static constexpr int all_done = dk_done + TP::BARS; // dV and dK are there
     static constexpr int drain = all_done + 1;     // [4]
     static constexpr int NBAR = drain + 4;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int TOTAL = 1024 + MISC + 16;
-    static constexpr bool TA = false;            // K and V in tensor memory
-    static constexpr uint32_t tS = 0, tP = HT * TS::TILES, tGV = tP + HT * TP::TILES, tGK = tGV + D, tK = tGK + D, tV = tK + D / 2;
-    static_assert(TA ? tV + D / 2 <= 512 : tK <= 512, "tensor memory budget");
+    static constexpr uint32_t tS = 0, tP = HT * TS::TILES, tGV = tP + HT * TP::TILES, tGK = tGV + D;
+    static_assert(tGK + D <= 512, "tensor memory budget");
+    static_assert(TOTAL <= 232448, "shared memory budget");
 };
 
 template <int D>
@@ -452,7 +455,6 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             int c = 1;
             if (i >= C::q_full && i < C::o_full) c = 1 + 32;
             if (i >= C::p_full && i < C::dv_done) c = NEL / 64;  // one a warp
-            if (i == C::a_full) c = NEL / 32;
             if ((i >= C::empty && i < C::zeroed) || i == C::all_done) c = 2;  // dV and dK
             mbar_init(&bar[i], c);
         }
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
                 __syncwarp();
             }
         } else if (warp == 16) {  // S^T
-            w.wait(&bar[C::TA ? C::a_full : C::kv_full], 0);
+            w.wait(&bar[C::kv_full], 0);
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
@@ -520,14 +522,11 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
                         if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     }
                     tc_fence_after();
-                    if (C::TA)
-                        mma_nt_ta<D, HT>(tmem + C::tS + HT * TS::tile(i), tmem + C::tK, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
-                    else
-                        mma_nt<D, HT>(tmem + C::tS + HT * TS::tile(i), sm + C::K, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
+                    mma_nt<D, HT>(tmem + C::tS + HT * TS::tile(i), sm + C::K, sm + C::Q + s * C::TILE + (x & 1) * kHalf);
                     commit(&bar[C::s_full + TS::bar(i)]);
                 }
         } else if (warp == 17) {  // dP^T
-            w.wait(&bar[C::TA ? C::a_full : C::kv_full], 0);
+            w.wait(&bar[C::kv_full], 0);
             for (int g = 0, i = 0; g < G; ++g)
                 for (int x = 0; x < n && !w.stopped(); ++x, ++i) {
                     const int j = g * nt + (x >> 1), s = j % NS;
@@ -537,10 +536,7 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
                         if (tail < BT) w.wait(&bar[C::zeroed + s], j / NS);
                     }
                     tc_fence_after();
-                    if (C::TA)
-                        mma_nt_ta<D, HT>(tmem + C::tP + HT * TP::tile(i), tmem + C::tV, sm + C::O + s * C::TILE + (x & 1) * kHalf);
-                    else
-                        mma_nt<D, HT>(tmem + C::tP + HT * TP::tile(i), sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
+                    mma_nt<D, HT>(tmem + C::tP + HT * TP::tile(i), sm + C::V, sm + C::O + s * C::TILE + (x & 1) * kHalf);
                     commit(&bar[C::dp_full + TP::bar(i)]);
                 }
         } else if (warp == 18) {  // dV
@@ -580,13 +576,6 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
         const int set = g >> 1, c0 = 32 * (g & 1);  // steps of this parity, these columns
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e);
-        if (C::TA) {  // groups 0, 1: halves of K's rows, 2, 3: of V's
-            w.wait(&bar[C::kv_full], 0);
-            row_to_tmem<D / 2>(tmem + lanes + (g < 2 ? C::tK : C::tV), sm + (g < 2 ? C::K : C::V), r, (g & 1) * (D / 2));
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(&bar[C::a_full], lane);
-        }
         TS ts(set);
         TP tp(set);
         int x0 = set, j0 = 0;  // step of a head's, and the head's first tile
