@@ -405,7 +405,8 @@ GDN_API int gdn_decode_step_gva(const void *q, const void *k, const void *v, con
  * softmax in fp32, its weights rounded to bf16 for the second product) or fp32 (CUDA cores, fp32
  * throughout).  scale finite and > 0.  A sequence may have length 0.  A non-finite k or v row may
  * also reach earlier rows of the same sequence within its block of 128 tokens, never another
- * sequence.  No workspace.  Errors as gdn_chunk_fwd.
+ * sequence.  Outputs must not overlap inputs.  No workspace.  Errors as gdn_chunk_fwd; too large a call
+ * (2^31 tokens, or 2^31 heads of 128-token blocks, an empty sequence counted as one) is an invalid argument.
  */
 GDN_API int gdn_attn_fwd(const void *q, const void *k, const void *v, void *out, float *lse, int B, int T, int Hq,
                          int Hk, int d, const int32_t *cu_seqlens, int dtype, float scale, void *stream);
@@ -417,7 +418,9 @@ GDN_API int gdn_attn_fwd(const void *q, const void *k, const void *v, void *out,
  *     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
  * with dk and dv summed over the query heads that share a key head, in a fixed order (no atomics:
  * a call repeats bit for bit).  Sums are fp32; with bf16 p and ds are rounded to bf16 for the
- * products they enter.  Rows behind cu[B] are left as they were.  Workspace:
+ * products they enter; the first 256 rows of a sequence form D_i as sum_j p_ij (dout_i . v_j), which the
+ * rounding of out does not touch.  Rows behind cu[B] are left as they were; a non-finite row also reaches
+ * gradients of rows within its block of 128 tokens that it should not, never another sequence.  Workspace:
  * gdn_attn_bwd_workspace_bytes(...) bytes of device memory, 256-byte aligned.  Errors as
  * gdn_attn_fwd.
  */

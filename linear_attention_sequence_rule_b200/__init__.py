@@ -971,7 +971,7 @@ def attn_fwd(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None, stream=No
     if T == 0 and cu_seqlens is not None:
         return out, lse
     _run(_lib.gdn_attn_fwd, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-         B, T, Hq, Hk, d, _ptr(cu_seqlens), code, d ** -0.5 if scale is None else scale)
+         B, T, Hq, Hk, d, _ptr(cu_seqlens), code, d ** -0.5 if scale is None else float(scale))
     return out, lse
 
 
@@ -1006,7 +1006,7 @@ def attn_bwd(q, k, v, out, lse, dout, cu_seqlens=None, scale=None, dq=None, dk=N
     keep, ws, wbytes = _scratch(workspace, need, stream, q)
     _run(_lib.gdn_attn_bwd, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
          dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, T, Hq, Hk, d, _ptr(cu_seqlens), code,
-         d ** -0.5 if scale is None else scale, ws, wbytes)
+         d ** -0.5 if scale is None else float(scale), ws, wbytes)
     return dq, dk, dv
 
 
@@ -1117,5 +1117,5 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=
     keep, ws, wbytes = _scratch(workspace, need, stream, q)
     _run(_lib.gdn_attn_decode, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
          v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(), out.data_ptr(), N, Hq, Hk, d, page, P,
-         max_blocks, code, d ** -0.5 if scale is None else scale, ws, wbytes)
+         max_blocks, code, d ** -0.5 if scale is None else float(scale), ws, wbytes)
     return out

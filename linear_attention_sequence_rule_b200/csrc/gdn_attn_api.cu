@@ -65,7 +65,8 @@ int check_prompt(const char *fn, int B, int T, int Hq, int Hk, int d, int varlen
     if (B < 1 || T < 0 || (!varlen && T < 1))
         return refuse(GDN_ERR_INVALID_ARGUMENT, "%s: B=%d T=%d (B >= 1; dense T >= 1)", fn, B, T);
     const long long tokens = varlen ? (long long)T : (long long)B * T;
-    if (tokens >= (1LL << 31) || tokens * Hq * d >= (1LL << 40) || B > (1 << 24))
+    const long long tiles = varlen ? T / 128 + (long long)B : (long long)B * ((T + 127LL) / 128);  // CTAs a head
+    if (tokens >= (1LL << 31) || tokens * Hq * d >= (1LL << 40) || B > (1 << 24) || tiles * Hq >= (1LL << 31))
         return refuse(GDN_ERR_INVALID_ARGUMENT, "%s: problem too large", fn);
     return GDN_OK;
 }

@@ -84,7 +84,7 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
 // Tiles per split of a context of `len` tokens over at most `n` splits; those past its end are empty.
 __device__ __forceinline__ int split_tiles(int len, int n)
 {
-    const int tiles = (len + TT - 1) / TT;
+    const int tiles = len > 0 ? (len - 1) / TT + 1 : 0;
     return max(1, (tiles + n - 1) / n);
 }
 
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(NW * 32, OCC)
     const int len = context_len(a.lens, n, a.max_blocks, a.page);
     const int per = split_tiles(len, splits);
     const int t0 = (int)min((long long)split * per * TT, (long long)len);
-    const int t1 = (int)min((long long)t0 + per * TT, (long long)len);
+    const int t1 = (int)min(t0 + (long long)per * TT, (long long)len);
     asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this grid's end
     if (t0 >= t1 && split > 0) return;  // split 0 writes the zeros of an empty context
 
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(NW * 32, OCC)
     __syncwarp();
 
     const int shift = __ffs(a.page) - 1;
-    const int tiles = (t1 - t0 + TT - 1) / TT;          // of this CTA; warp w takes tiles w, w + 4, ...
+    const int tiles = t1 > t0 ? (t1 - t0 - 1) / TT + 1 : 0;  // of this CTA; warp w takes tiles w, w + 4, ...
     const int mine = tiles > warp ? (tiles - warp + NW - 1) / NW : 0;
     const int32_t *table = a.table + (int64_t)n * a.max_blocks;
     const bool small = a.page < TT;

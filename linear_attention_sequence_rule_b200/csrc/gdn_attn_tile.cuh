@@ -17,7 +17,8 @@ struct AttnTile {
 // launch does not end with a long one alone.  Dense calls have B ceil(T / rows) tiles; a packed launch
 // has at most T / rows + B, and the tiles past the last one are empty.  With more than 128 sequences
 // (each lane holds four lengths; many sequences of a launch's size are short ones) packed tiles go
-// sequence by sequence, each from its last block on.  Called by whole warps.
+// sequence by sequence, each from its last block on: sequence s has the tiles from cu[s] / rows + s on, since
+// len / rows rounded up is at most cu[s + 1] / rows - cu[s] / rows + 1.  Called by whole warps.
 __device__ __forceinline__ AttnTile attn_tile(const int32_t *__restrict__ cu, int B, int T, int rows, int index)
 {
     AttnTile r;
@@ -30,7 +31,6 @@ __device__ __forceinline__ AttnTile attn_tile(const int32_t *__restrict__ cu, in
         return r;
     }
     const int lane = threadIdx.x & 31;
-    int base = 0;
     r.seq = -1;
     r.block = r.len = 0;
     r.t0 = 0;
@@ -72,33 +72,23 @@ __device__ __forceinline__ AttnTile attn_tile(const int32_t *__restrict__ cu, in
         r.len = min(cu[r.seq + 1], T) - (int)r.t0;
         return r;
     }
-    for (int s0 = 0; s0 < B; s0 += 32) {
-        const int s = s0 + lane;
-        int a = 0, len = 0;
-        if (s < B) {
-            a = cu[s];
-            len = max(0, min(cu[s + 1], T) - a);
-            if (a < 0) len = 0;
-        }
-        const int n = (len + rows - 1) / rows;
-        int incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        const int rel = index - base;
-        const unsigned hit = __ballot_sync(0xffffffffu, rel >= incl - n && rel < incl);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            r.seq = s0 + src;
-            r.block = __shfl_sync(0xffffffffu, incl - 1 - rel, src);
-            r.len = __shfl_sync(0xffffffffu, len, src);
-            r.t0 = __shfl_sync(0xffffffffu, a, src);
-            return r;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+    // largest s with cu[s] / rows + s <= index: 32 of them looked at at once
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int stride = (hi - lo + 31) >> 5, s = lo + lane * stride;
+        const unsigned before = __ballot_sync(0xffffffffu, s < hi && max(cu[s], 0) / rows + s <= index);
+        const int c = before == 0xffffffffu ? 32 : __ffs(~before) - 1;
+        lo += max(0, c - 1) * stride;
+        hi = min(hi, lo + stride);
     }
+    const int a = cu[lo], len = min(cu[lo + 1], T) - a;
+    if (a < 0 || len <= 0) return r;
+    const int n = (len + rows - 1) / rows, rel = index - a / rows - lo;
+    if (rel < 0 || rel >= n) return r;
+    r.seq = lo;
+    r.block = n - 1 - rel;
+    r.len = len;
+    r.t0 = a;
     return r;
 }
 

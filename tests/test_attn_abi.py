@@ -25,7 +25,8 @@ SHARED = [(dict(dtype=7), UNS), (dict(d=96), UNS), (dict(d=256), UNS), (dict(Hq=
           (dict(T=-1, cu_seqlens=FAKE), BAD), (dict(B=1 << 16, T=1 << 16), BAD), (dict(T=1 << 30, Hq=64), BAD),
           (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD), (dict(scale=float("nan")), BAD),
           (dict(scale=float("inf")), BAD), (dict(q=None), BAD), (dict(out=None), BAD), (dict(v=FAKE + 8), BAD),
-          (dict(cu_seqlens=FAKE + 4), BAD), (dict(lse=FAKE + 4), BAD)]
+          (dict(cu_seqlens=FAKE + 4), BAD), (dict(lse=FAKE + 4), BAD),
+          (dict(B=1 << 24, Hq=256, cu_seqlens=FAKE), BAD)]
 
 
 @pytest.mark.parametrize("kw,code", SHARED)
@@ -57,7 +58,8 @@ PLAN = dict(lens=FAKE, added=FAKE, block_table=FAKE, free_list=FAKE, free_head=F
 @pytest.mark.parametrize("kw,code", [(dict(page=48), UNS), (dict(page=0), UNS), (dict(N=16385), UNS), (dict(N=0), BAD),
                                      (dict(max_blocks=0), BAD), (dict(max_blocks=1 << 25), BAD),
                                      (dict(num_free=-1), BAD), (dict(rows=-1), BAD), (dict(lens=None), BAD),
-                                     (dict(slots=None), BAD), (dict(free_list=None), BAD), (dict(status=None), BAD),
+                                     (dict(slots=None), BAD), (dict(slots=FAKE + 4), BAD), (dict(free_head=FAKE + 2), BAD),
+                                     (dict(status=FAKE + 1), BAD), (dict(free_list=None), BAD), (dict(status=None), BAD),
                                      (dict(block_table=FAKE + 4), BAD)])
 def test_cache_plan(kw, code):
     assert call(gdn.gdn_cache_plan, PLAN, kw) == code

@@ -74,7 +74,7 @@ def test_packed(lengths, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("B", [128, 129, 300])
+@pytest.mark.parametrize("B", [128, 129, 300, 1025, 2500])
 def test_packed_many_sequences(B, dtype):
     lengths = np.random.RandomState(B).randint(0, 9, B)
     lengths[[1, B // 2, B - 2]] = [200, 333, 129]
