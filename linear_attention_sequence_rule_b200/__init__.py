@@ -6,11 +6,14 @@ PyTorch provides device memory and streams.  The binding has two layers:
 * ``gdn_chunk_fwd``, ``gdn_chunk_fwd_noalloc``, ``gdn_chunk_fwd_host``, ``gdn_phase_fwd``,
   ``gdn_phase_rowdecay_fwd``, ``gdn_decode_step``,
   ``gdn_chunk_fwd_workspace_bytes``, ``gdn_chunk_fwd_host_workspace_bytes``,
+  ``gdn_attn_fwd``, ``gdn_attn_bwd``, ``gdn_attn_bwd_workspace_bytes``, ``gdn_cache_plan``, ``gdn_cache_append``,
+  ``gdn_attn_decode``, ``gdn_attn_decode_workspace_bytes``,
   ``gdn_status_string``, ``gdn_last_error``, ``gdn_version`` -- the C-ABI entry points of
   ``include/gdn.h`` with the same names and arguments (pointers as Python ints);
 * ``chunk_fwd``, ``chunk_fwd_host``, ``chunk_fwd_fused``, ``chunk_fwd_gva``, ``chunk_bwd``,
   ``chunk_bwd_fused``, ``chunk_bwd_gva``, ``phase_fwd``, ``phase_rowdecay_fwd``, ``phase_bwd``, ``decode_step``,
-  ``decode_step_fused`` and ``decode_step_gva`` --
+  ``decode_step_fused``, ``decode_step_gva``, ``attn_fwd``, ``attn_bwd``, ``cache_plan``, ``cache_append`` and
+  ``attn_decode`` --
   the same calls taking torch tensors; they check shapes,
   devices and dtypes, allocate outputs with torch when none are given, and raise ``GdnError``
   on a non-zero status.

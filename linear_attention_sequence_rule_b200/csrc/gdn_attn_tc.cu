@@ -84,17 +84,38 @@ __global__ void __launch_bounds__(NTH, 1)
     const int n0 = (min(at.len, q0 + BT) + HT - 1) / HT, n1 = rows > BT ? (min(at.len, q0 + 2 * BT) + HT - 1) / HT : 0;
     const int tiles = (max(n0, n1) + 1) / 2;
 
-    if (tid == 0) {
-        for (int i = 0; i < C::NBAR; ++i) {
+    auto load_k = [&](int j) {
+        const int s = j % NS;
+        mbar_arrive_expect_tx(&bar[C::k_full + s], C::TILE);
+        load_tile<D>(sm + C::K + s * C::TILE, &tmK, &bar[C::k_full + s], hk, (int)at.t0 + j * BT);
+    };
+    auto load_v = [&](int j) {
+        const int s = j % NS;
+        mbar_arrive_expect_tx(&bar[C::v_full + s], C::TILE);
+        load_tile<D>(sm + C::V + s * C::TILE, &tmV, &bar[C::v_full + s], hk, (int)at.t0 + j * BT);
+    };
+    if (warp == 10) {  // the first loads are under way before the rest is set up
+        for (int i = lane; i < C::NBAR; i += 32) {
             int n = 1;
             if ((i >= C::k_empty && i < C::v_full) || (i >= C::v_empty && i < C::v_zeroed)) n = n1 ? 2 : 1;
             if (i >= C::p_full && i < C::pv_done) n = BT / 32;  // one a warp
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
-        *abort_flag = 0;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            *abort_flag = 0;
+            for (int t = 0; t < (n1 ? 2 : 1); ++t) {
+                mbar_arrive_expect_tx(&bar[C::q_full + t], C::TILE);
+                load_tile<D>(sm + C::Q + t * C::TILE, &tmQ, &bar[C::q_full + t], h, (int)at.t0 + q0 + t * BT);
+                if (t == 0) load_k(0);
+            }
+            load_v(0);
+        }
+        __syncwarp();
     }
-    if (warp == 10) {
+    if (warp == 11) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -109,20 +130,14 @@ __global__ void __launch_bounds__(NTH, 1)
         if (warp == 10) {
         // ---- loads ----
         if (lane == 0) {
-            for (int t = 0; t < (n1 ? 2 : 1); ++t) {
-                mbar_arrive_expect_tx(&bar[C::q_full + t], C::TILE);
-                load_tile<D>(sm + C::Q + t * C::TILE, &tmQ, &bar[C::q_full + t], h, (int)at.t0 + q0 + t * BT);
-            }
-            for (int j = 0; j < tiles && !w.aborted(); ++j) {
+            for (int j = 1; j < tiles && !w.aborted(); ++j) {
                 const int s = j % NS;
                 if (j >= NS) w.wait(&bar[C::k_empty + s], j / NS - 1);
                 if (w.aborted()) break;
-                mbar_arrive_expect_tx(&bar[C::k_full + s], C::TILE);
-                load_tile<D>(sm + C::K + s * C::TILE, &tmK, &bar[C::k_full + s], hk, (int)at.t0 + j * BT);
+                load_k(j);
                 if (j >= NS) w.wait(&bar[C::v_empty + s], j / NS - 1);
                 if (w.aborted()) break;
-                mbar_arrive_expect_tx(&bar[C::v_full + s], C::TILE);
-                load_tile<D>(sm + C::V + s * C::TILE, &tmV, &bar[C::v_full + s], hk, (int)at.t0 + j * BT);
+                load_v(j);
             }
         }
         __syncwarp();
@@ -277,7 +292,7 @@ __global__ void __launch_bounds__(NTH, 1)
             }
     tc_fence_before();
     __syncthreads();
-    if (warp == 10) {
+    if (warp == 11) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

@@ -166,14 +166,34 @@ __global__ void __launch_bounds__(NTH, 1)
     const int passes = exact ? 2 : 1, steps = passes * n;  // the first of two passes forms D
     const int64_t row0 = at.t0 + at.block * BT;
 
-    if (tid == 0) {
-        for (int i = 0; i < C::NBAR; ++i)
+    auto load_k = [&](int i, int j) {
+        const int s = i % NK;
+        mbar_arrive_expect_tx(&bar[C::k_full + s], C::TILE);
+        load_tile<D>(sm + C::K + s * C::TILE, &tmK, &bar[C::k_full + s], hk, (int)at.t0 + j * BT);
+    };
+    auto load_v = [&](int i, int j) {
+        const int s = i % NV;
+        mbar_arrive_expect_tx(&bar[C::v_full + s], C::TILE);
+        load_tile<D>(sm + C::V + s * C::TILE, &tmV, &bar[C::v_full + s], hk, (int)at.t0 + j * BT);
+    };
+    if (warp == 19) {  // the first loads are under way before the rest is set up
+        for (int i = lane; i < C::NBAR; i += 32)
             mbar_init(&bar[i], i == C::a_full ? NEL / 32 : i >= C::s_free && i < C::dq_done ? NEL / 64  // one a warp
                                : C::BOTH && i >= C::s_full && i < C::dp_full ? 2 : 1);
         fence_mbar_init();
-        *abort_flag = 0;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            *abort_flag = 0;
+            mbar_arrive_expect_tx(&bar[C::q_full], 2 * C::TILE);
+            load_tile<D>(sm + C::Q, &tmQ, &bar[C::q_full], h, (int)row0);
+            load_tile<D>(sm + C::O, &tmO, &bar[C::q_full], h, (int)row0);
+            load_k(0, 0);
+            load_v(0, 0);
+        }
+        __syncwarp();
     }
-    if (warp == 19) {
+    if (warp == 16) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -186,24 +206,13 @@ __global__ void __launch_bounds__(NTH, 1)
     if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 19) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar[C::q_full], 2 * C::TILE);
-                load_tile<D>(sm + C::Q, &tmQ, &bar[C::q_full], h, (int)row0);
-                load_tile<D>(sm + C::O, &tmO, &bar[C::q_full], h, (int)row0);
-            }
             for (int i = 0; i < passes * nt; ++i) {
                 const int sk = i % NK, sv = i % NV, j = i % nt;
-                if (lane == 0) {
+                if (lane == 0 && i > 0) {
                     if (i >= NK) w.wait(&bar[C::k_empty + sk], i / NK - 1);
-                    if (!w.aborted()) {
-                        mbar_arrive_expect_tx(&bar[C::k_full + sk], C::TILE);
-                        load_tile<D>(sm + C::K + sk * C::TILE, &tmK, &bar[C::k_full + sk], hk, (int)at.t0 + j * BT);
-                    }
+                    if (!w.aborted()) load_k(i, j);
                     if (i >= NV) w.wait(&bar[C::v_empty + sv], i / NV - 1);
-                    if (!w.aborted()) {
-                        mbar_arrive_expect_tx(&bar[C::v_full + sv], C::TILE);
-                        load_tile<D>(sm + C::V + sv * C::TILE, &tmV, &bar[C::v_full + sv], hk, (int)at.t0 + j * BT);
-                    }
+                    if (!w.aborted()) load_v(i, j);
                 }
                 __syncwarp();
                 if (w.stopped()) break;
@@ -276,18 +285,23 @@ __global__ void __launch_bounds__(NTH, 1)
         const bool live = r < rows;
         const float nl = live ? -lse[(row0 + r) * Hq + h] * kLog2e : 0.f;
         float nd = 0.f;
+        uint4 ov[D / 32];  // this thread's quarter of the row of out
+        if (!exact && live) {
+            const uint4 *o = reinterpret_cast<const uint4 *>(out + ((row0 + r) * Hq + h) * D) + g * (D / 32);
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) ov[u] = o[u];
+        }
         w.wait(&bar[C::q_full], 0);  // groups 0, 1: halves of Q's rows, 2, 3: of dO's
         row_to_tmem<D / 2>(tmem + lanes + (g < 2 ? C::tQ : C::tO), sm + (g < 2 ? C::Q : C::O), r, (g & 1) * (D / 2));
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&bar[C::a_full], lane);
-        if (!exact) {  // D from out: this thread's quarter of the row
+        if (!exact) {  // D from out
             if (live) {
-                const uint4 *o = reinterpret_cast<const uint4 *>(out + ((row0 + r) * Hq + h) * D) + g * (D / 32);
 #pragma unroll
                 for (int u = 0; u < D / 32; ++u) {
                     const int x = g * (D / 32) + u;
-                    const uint4 a = o[u], b = *reinterpret_cast<const uint4 *>(sm + C::O + (x >> 3) * kSub + r * 128 +
+                    const uint4 a = ov[u], b = *reinterpret_cast<const uint4 *>(sm + C::O + (x >> 3) * kSub + r * 128 +
                                                                                (((x & 7) ^ (r & 7)) << 4));
                     const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -383,7 +397,7 @@ __global__ void __launch_bounds__(NTH, 1)
     if (w.aborted() && warp == 19 && lane == 0) drain_loads(bar, C::q_full, 1 + NK + NV);
     tc_fence_before();
     __syncthreads();
-    if (warp == 19) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -450,8 +464,8 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
     const int tail = at.len - (blocks - 1) * BT;   // queries of the last block
     const int64_t row0 = at.t0 + kb * BT;
 
-    if (tid == 0) {
-        for (int i = 0; i < C::NBAR; ++i) {
+    if (warp == 20) {  // the first loads are under way before the rest is set up
+        for (int i = lane; i < C::NBAR; i += 32) {
             int c = 1;
             if (i >= C::q_full && i < C::o_full) c = 1 + 32;
             if (i >= C::p_full && i < C::dv_done) c = NEL / 64;  // one a warp
@@ -459,9 +473,21 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             mbar_init(&bar[i], c);
         }
         fence_mbar_init();
-        *abort_flag = 0;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            *abort_flag = 0;
+            mbar_arrive_expect_tx(&bar[C::kv_full], 2 * C::TILE);
+            load_tile<D>(sm + C::K, &tmK, &bar[C::kv_full], hk, (int)row0);
+            load_tile<D>(sm + C::V, &tmV, &bar[C::kv_full], hk, (int)row0);
+            mbar_arrive_expect_tx(&bar[C::q_full], C::TILE);
+            load_tile<D>(sm + C::Q, &tmQ, &bar[C::q_full], hk * G, (int)row0);
+            mbar_arrive_expect_tx(&bar[C::o_full], C::TILE);
+            load_tile<D>(sm + C::O, &tmO, &bar[C::o_full], hk * G, (int)row0);
+        }
+        __syncwarp();
     }
-    if (warp == 20) {
+    if (warp == 16) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -475,17 +501,12 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
     if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 20) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar[C::kv_full], 2 * C::TILE);
-                load_tile<D>(sm + C::K, &tmK, &bar[C::kv_full], hk, (int)row0);
-                load_tile<D>(sm + C::V, &tmV, &bar[C::kv_full], hk, (int)row0);
-            }
             for (int i = 0; i < G * nt; ++i) {
                 const int s = i % NS, h = hk * G + i / nt, qb = kb + i % nt;
                 if (i >= NS) w.wait(&bar[C::empty + s], i / NS - 1);
                 if (w.stopped()) break;
                 const int64_t q0 = at.t0 + qb * BT;
-                if (lane == 0) {
+                if (lane == 0 && i > 0) {
                     mbar_arrive_expect_tx(&bar[C::q_full + s], C::TILE);
                     load_tile<D>(sm + C::Q + s * C::TILE, &tmQ, &bar[C::q_full + s], h, (int)q0);
                     mbar_arrive_expect_tx(&bar[C::o_full + s], C::TILE);
@@ -649,7 +670,7 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 20) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
