@@ -161,7 +161,7 @@ template <int D, int RPT> constexpr int fwd_smem()
 template <int D, int RPT>
 __global__ void __launch_bounds__(NT) attn_fwd_simt(const float *__restrict__ q, const float *__restrict__ k,
                                                     const float *__restrict__ v, float *__restrict__ out,
-                                                    float *__restrict__ lse, const int32_t *__restrict__ cu, int B,
+                                                    float *__restrict__ lse, const int32_t *__restrict__ cu, FastDiv B,
                                                     int Tn, int Hq, int Hk, float scale2)
 {
     constexpr int BM = 16 * RPT;
@@ -305,7 +305,7 @@ template <int D>
 __global__ void __launch_bounds__(NT) attn_bwd_dq_simt(const float *__restrict__ q, const float *__restrict__ k,
                                                        const float *__restrict__ v, const float *__restrict__ dout,
                                                        const float *__restrict__ lse, const float *__restrict__ dot,
-                                                       float *__restrict__ dq, const int32_t *__restrict__ cu, int B,
+                                                       float *__restrict__ dq, const int32_t *__restrict__ cu, FastDiv B,
                                                        int Tn, int Hq, int Hk, float scale)
 {
     extern __shared__ float sm[];
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(NT) attn_bwd_dkv_simt(const float *__restrict_
                                                         const float *__restrict__ v, const float *__restrict__ dout,
                                                         const float *__restrict__ lse, const float *__restrict__ dot,
                                                         float *__restrict__ dk, float *__restrict__ dv,
-                                                        const int32_t *__restrict__ cu, int B, int Tn, int Hq, int Hk,
+                                                        const int32_t *__restrict__ cu, FastDiv B, int Tn, int Hq, int Hk,
                                                         float scale)
 {
     extern __shared__ float sm[];
@@ -423,8 +423,8 @@ template <int D, int RPT> cudaError_t run_fwd(const AttnArgs &a, cudaStream_t st
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)attn_tiles(a.cu, a.B, a.T, 16 * RPT), a.Hq);
-    kern<<<grid, NT, smem, st>>>((const float *)a.q, (const float *)a.k, (const float *)a.v, (float *)a.out, a.lse, a.cu, a.B, a.T,
-                                 a.Hq, a.Hk, a.scale * kLog2e);
+    kern<<<grid, NT, smem, st>>>((const float *)a.q, (const float *)a.k, (const float *)a.v, (float *)a.out, a.lse, a.cu,
+                                 FastDiv(a.B), a.T, a.Hq, a.Hk, a.scale * kLog2e);
     return cudaGetLastError();
 }
 
@@ -441,13 +441,13 @@ template <int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t st)
                                                                                  dot, rows, a.cu, a.B, a.Hq);
     const unsigned tiles = (unsigned)attn_tiles(a.cu, a.B, a.T, 64);
     attn_bwd_dq_simt<D><<<dim3(tiles, a.Hq), NT, smem, st>>>((const float *)a.q, (const float *)a.k, (const float *)a.v,
-                                                                (const float *)a.dout, a.lse, dot, (float *)a.dq, a.cu, a.B,
-                                                                a.T, a.Hq, a.Hk, a.scale);
+                                                                (const float *)a.dout, a.lse, dot, (float *)a.dq, a.cu,
+                                                                FastDiv(a.B), a.T, a.Hq, a.Hk, a.scale);
     const bool shared = a.Hq > a.Hk;
     float *pk = dot + (rows + 63) / 64 * 64, *pv = pk + rows * D;  // behind D, if heads are shared
     attn_bwd_dkv_simt<D><<<dim3(tiles, a.Hq), NT, smem, st>>>(
         (const float *)a.q, (const float *)a.k, (const float *)a.v, (const float *)a.dout, a.lse, dot,
-        shared ? pk : (float *)a.dk, shared ? pv : (float *)a.dv, a.cu, a.B, a.T, a.Hq, a.Hk, a.scale);
+        shared ? pk : (float *)a.dk, shared ? pv : (float *)a.dv, a.cu, FastDiv(a.B), a.T, a.Hq, a.Hk, a.scale);
     if (shared) {
         const int64_t n4 = rows / a.Hq * a.Hk * (D / 4);
         attn_bwd_add_heads<<<dim3((unsigned)((n4 + NT - 1) / NT), 2), NT, 0, st>>>(

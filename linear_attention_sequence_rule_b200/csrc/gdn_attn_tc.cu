@@ -64,7 +64,8 @@ template <int D>
 __global__ void __launch_bounds__(NTH, 1)
     attn_fwd_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
-                const int32_t *__restrict__ cu, int B, int T, int Hq, int Hk, float scale2)
+                const int32_t *__restrict__ cu, FastDiv B, int T, FastDiv heads, FastDiv group,
+                float scale2)
 {
     using C = FwdCfg<D>;
     constexpr int NS = C::NS;
@@ -76,9 +77,10 @@ __global__ void __launch_bounds__(NTH, 1)
     const Waits w{abort_flag, &g_attn_fwd_error};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const AttnTile at = attn_tile(cu, B, T, 2 * BT, blockIdx.x / Hq);
+    const int Hq = (int)heads.d, index = heads.div(blockIdx.x);
+    const AttnTile at = attn_tile(cu, B, T, 2 * BT, index);
     if (at.seq < 0) return;
-    const int h = blockIdx.x % Hq, hk = h / (Hq / Hk);
+    const int h = blockIdx.x - index * Hq, hk = group.div(h);
     const int q0 = at.block * 2 * BT, rows = at.len - q0;  // rows of this CTA's queries that exist
     // steps of the two tiles (the keys their rows see), and key tiles of 128
     const int n0 = (min(at.len, q0 + BT) + HT - 1) / HT, n1 = rows > BT ? (min(at.len, q0 + 2 * BT) + HT - 1) / HT : 0;
@@ -309,7 +311,8 @@ template <int D> cudaError_t run_fwd(const AttnArgs &a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const long tiles = attn_tiles(a.cu, a.B, a.T, 2 * BT);
     attn_fwd_tc<D><<<(unsigned)(tiles * a.Hq), NTH, C::TOTAL, st>>>(mq, mk, mv, static_cast<__nv_bfloat16 *>(a.out), a.lse,
-                                                                   a.cu, a.B, a.T, a.Hq, a.Hk, a.scale * kLog2e);
+                                                                   a.cu, FastDiv(a.B), a.T, FastDiv(a.Hq), FastDiv(a.Hq / a.Hk),
+                                                                   a.scale * kLog2e);
     return cudaGetLastError();
 }
 

@@ -226,7 +226,7 @@ __device__ __forceinline__ void store_rows(uint32_t t, float f, unsigned char *b
 {
     constexpr int UN = NC / 8;  // 16-byte units a row
     const int r = 32 * warp + lane, u0 = c0 / 8;
-#pragma unroll
+#pragma unroll 1  // (code that a CTA runs once comes from memory, line by line)
     for (int x = 0; x < NC / 32; ++x) {
         float o[32];
         tmem_ld32(t + c0 + 32 * x, o);

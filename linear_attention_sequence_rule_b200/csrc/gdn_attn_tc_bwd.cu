@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(NTH, 1)
     attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                    const __nv_bfloat16 *__restrict__ out, const float *__restrict__ lse, __nv_bfloat16 *__restrict__ dq,
-                   float *__restrict__ nlse, float *__restrict__ ndot, const int32_t *__restrict__ cu, int B, int T,
-                   int Hq, int Hk, float scale, int64_t tokens)
+                   float *__restrict__ nlse, float *__restrict__ ndot, const int32_t *__restrict__ cu, FastDiv B, int T,
+                   FastDiv heads, FastDiv group, float scale, int64_t tokens)
 {
     using C = DqCfg<D>;
     using TS = typename C::TS;
@@ -156,9 +156,10 @@ __global__ void __launch_bounds__(NTH, 1)
     const Waits w{abort_flag, &g_attn_bwd_error};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const AttnTile at = attn_tile(cu, B, T, BT, blockIdx.x / Hq);
+    const int Hq = (int)heads.d, index = heads.div(blockIdx.x);
+    const AttnTile at = attn_tile(cu, B, T, BT, index);
     if (at.seq < 0) return;
-    const int h = blockIdx.x % Hq, hk = h / (Hq / Hk);
+    const int h = blockIdx.x - index * Hq, hk = group.div(h);
     const int rows = at.len - at.block * BT;       // that exist
     const int n = (min(at.len, (at.block + 1) * BT) + HT - 1) / HT;  // steps of a pass
     const int nt = (n + 1) / 2;                    // key tiles of a pass
@@ -285,46 +286,59 @@ __global__ void __launch_bounds__(NTH, 1)
         const bool live = r < rows;
         const float nl = live ? -lse[(row0 + r) * Hq + h] * kLog2e : 0.f;
         float nd = 0.f;
-        uint4 ov[D / 32];  // this thread's quarter of the row of out
-        if (!exact && live) {
-            const uint4 *o = reinterpret_cast<const uint4 *>(out + ((row0 + r) * Hq + h) * D) + g * (D / 32);
+        // D from out: a warp has 8 rows, D / 8 lanes a row
+        constexpr int LR = D / 8;
+        uint4 ov[D / 32];
+        const int ro = 8 * warp + lane / LR, un = lane % LR;
+        if (!exact) {
 #pragma unroll
-            for (int u = 0; u < D / 32; ++u) ov[u] = o[u];
+            for (int u = 0; u < D / 32; ++u) {
+                const int x = ro + u * (32 / LR);
+                if (x < rows) ov[u] = *(reinterpret_cast<const uint4 *>(out + ((row0 + x) * Hq + h) * D) + un);
+            }
         }
         w.wait(&bar[C::q_full], 0);  // groups 0, 1: halves of Q's rows, 2, 3: of dO's
         row_to_tmem<D / 2>(tmem + lanes + (g < 2 ? C::tQ : C::tO), sm + (g < 2 ? C::Q : C::O), r, (g & 1) * (D / 2));
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&bar[C::a_full], lane);
-        if (!exact) {  // D from out
-            if (live) {
-#pragma unroll
-                for (int u = 0; u < D / 32; ++u) {
-                    const int x = g * (D / 32) + u;
-                    const uint4 a = ov[u], b = *reinterpret_cast<const uint4 *>(sm + C::O + (x >> 3) * kSub + r * 128 +
-                                                                               (((x & 7) ^ (r & 7)) << 4));
-                    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        nd = fmaf(__uint_as_float(av[e] << 16), -__uint_as_float(bv[e] << 16), nd);
-                        nd = fmaf(__uint_as_float(av[e] & 0xffff0000u), -__uint_as_float(bv[e] & 0xffff0000u), nd);
-                    }
-                }
-            }
-        }
-        auto join = [&]() {  // the four parts of D; for the key side too
-            if (g >= 2) red[(g - 2) * BT + r] = nd;
-            named_bar(1, NEL);
-            if (g < 2) red[g * BT + r] += nd;
-            named_bar(1, NEL);
-            nd = red[r] + red[BT + r];
+        auto known = [&]() {  // for the key side too
             if (g == 0 && live) {
                 nlse[(int64_t)h * tokens + row0 + r] = nl;
                 ndot[(int64_t)h * tokens + row0 + r] = nd;
             }
         };
+        if (!exact) {
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) {
+                const int x = ro + u * (32 / LR);
+                float acc = 0.f;
+                if (x < rows) {
+                    const uint4 b = *reinterpret_cast<const uint4 *>(sm + C::O + (un >> 3) * kSub + x * 128 + (((un & 7) ^ (x & 7)) << 4));
+                    const uint32_t av[4] = {ov[u].x, ov[u].y, ov[u].z, ov[u].w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc = fmaf(__uint_as_float(av[e] << 16), -__uint_as_float(bv[e] << 16), acc);
+                        acc = fmaf(__uint_as_float(av[e] & 0xffff0000u), -__uint_as_float(bv[e] & 0xffff0000u), acc);
+                    }
+                }
+#pragma unroll
+                for (int o = LR / 2; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                if (un == 0) red[x] = acc;
+            }
+            named_bar(1, NEL);
+            nd = red[r];
+            known();
+        }
+        auto join = [&]() {  // the four parts of D from the first pass
+            if (g >= 2) red[(g - 2) * BT + r] = nd;
+            named_bar(1, NEL);
+            if (g < 2) red[g * BT + r] += nd;
+            named_bar(1, NEL);
+            nd = red[r] + red[BT + r];
+            known();
+        };
         bool joined = !exact;
-        if (joined) join();
         const uint64_t sc2 = pack2(scale * kLog2e, scale * kLog2e), nl2 = pack2(nl, nl);
         TS ts(set);
         TP tp(set);
@@ -437,7 +451,7 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
     attn_bwd_dkv_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const float *__restrict__ nlse, const float *__restrict__ ndot, __nv_bfloat16 *__restrict__ dk,
-                    __nv_bfloat16 *__restrict__ dv, const int32_t *__restrict__ cu, int B, int T, int Hq, int Hk,
+                    __nv_bfloat16 *__restrict__ dv, const int32_t *__restrict__ cu, FastDiv B, int T, FastDiv heads, int G,
                     float scale, int64_t tokens)
 {
     using C = DkvCfg<D>;
@@ -452,9 +466,10 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
     const Waits w{abort_flag, &g_attn_bwd_error};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const AttnTile at = attn_tile(cu, B, T, BT, blockIdx.x / Hk);
+    const int Hk = (int)heads.d, index = heads.div(blockIdx.x);
+    const AttnTile at = attn_tile(cu, B, T, BT, index);
     if (at.seq < 0) return;
-    const int hk = blockIdx.x % Hk, G = Hq / Hk;
+    const int hk = blockIdx.x - index * Hk;
     const int blocks = (at.len + BT - 1) / BT;
     const int kb = blocks - 1 - at.block;          // the first key blocks see the most queries
     const int n = (at.len - kb * BT + HT - 1) / HT;  // steps per head
@@ -691,12 +706,13 @@ template <int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     float *nlse = static_cast<float *>(a.workspace), *ndot = nlse + tokens * a.Hq;
     const long tiles = attn_tiles(a.cu, a.B, a.T, BT);
+    const int G = a.Hq / a.Hk;
     attn_bwd_dq_tc<D><<<(unsigned)(tiles * a.Hq), NTH, A::TOTAL, st>>>(
         mq, mk, mv, mo, static_cast<const __nv_bfloat16 *>(a.out), a.lse, static_cast<__nv_bfloat16 *>(a.dq), nlse, ndot,
-        a.cu, a.B, a.T, a.Hq, a.Hk, a.scale, tokens);
+        a.cu, FastDiv(a.B), a.T, FastDiv(a.Hq), FastDiv(G), a.scale, tokens);
     attn_bwd_dkv_tc<D><<<(unsigned)(tiles * a.Hk), NTH_KEY, Bc::TOTAL, st>>>(
-        mq, mk, mv, mo, nlse, ndot, static_cast<__nv_bfloat16 *>(a.dk), static_cast<__nv_bfloat16 *>(a.dv), a.cu, a.B, a.T,
-        a.Hq, a.Hk, a.scale, tokens);
+        mq, mk, mv, mo, nlse, ndot, static_cast<__nv_bfloat16 *>(a.dk), static_cast<__nv_bfloat16 *>(a.dv), a.cu, FastDiv(a.B),
+        a.T, FastDiv(a.Hk), G, a.scale, tokens);
     return cudaGetLastError();
 }
 

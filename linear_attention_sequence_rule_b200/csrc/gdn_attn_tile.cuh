@@ -5,6 +5,19 @@
 
 namespace gdn {
 
+// Division of n < 2^31 by a number known at launch: with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1,
+// n / d = (floor(m n / 2^32) + n) / 2^l (Granlund and Montgomery 1994).  A CTA starts with a handful of divisions by
+// heads and sequences, some 100 cycles each in their general form.
+struct FastDiv {
+    uint32_t d, m, l;
+    explicit FastDiv(int by) : d((uint32_t)by), m(0), l(0)
+    {
+        while ((1ull << l) < d) ++l;
+        m = (uint32_t)((((1ull << l) - d) << 32) / d + 1);
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> l); }
+};
+
 struct AttnTile {
     int seq;     // -1: this tile does not exist
     int block;   // block of `rows` tokens within the sequence
@@ -19,13 +32,15 @@ struct AttnTile {
 // (each lane holds four lengths; many sequences of a launch's size are short ones) packed tiles go
 // sequence by sequence, each from its last block on: sequence s has the tiles from cu[s] / rows + s on, since
 // len / rows rounded up is at most cu[s + 1] / rows - cu[s] / rows + 1.  Called by whole warps.
-__device__ __forceinline__ AttnTile attn_tile(const int32_t *__restrict__ cu, int B, int T, int rows, int index)
+__device__ __forceinline__ AttnTile attn_tile(const int32_t *__restrict__ cu, const FastDiv &by, int T, int rows, int index)
 {
+    const int B = (int)by.d;
     AttnTile r;
     if (!cu) {
         const int n = (T + rows - 1) / rows;
-        r.seq = index % B;
-        r.block = n - 1 - index / B;
+        const int turn = by.div(index);
+        r.seq = index - turn * B;
+        r.block = n - 1 - turn;
         r.len = T;
         r.t0 = (int64_t)r.seq * T;
         return r;
