@@ -19,15 +19,18 @@
 // Both kernels work in steps of 64 keys (query side) or 64 queries (key side): 128 x 64 tiles of S and
 // dP in tensor memory beside the gradients, two of each at d = 128 (2 x 64 + 2 x 64 + 256 columns) and three at
 // d = 64, so that the products of the next steps run while a step's elements are worked on.  What bounds them is
-// the chain of waits between products and elements: at d = 64 a query-side step takes 900 cycles, of which 512
-// are its exponentials; without products and element-wise work it still takes 540.  Steps of 128 with one dP (or,
-// on the key side, one S) tile spend 1900 cycles each on it, and half again as many element-wise warps
-// change nothing.
+// the chain of waits between products and elements: at d = 64 (16384 tokens, 16 heads) the query side takes
+// 0.88 ms, 0.80 without its exponentials, 0.75 without any product, and still 0.53 without both and the rest of the
+// element-wise work.  Steps of 128 with one dP (or, on the key side, one S) tile spend half their time on it, and
+// half again as many element-wise warps change nothing.
 // A product 64 wide of two shared operands takes 48 cycles for 32 cycles' work, so the query side moves Q and dO
 // to tensor memory.  The key side leaves K and V in shared memory: at d = 64 a third tile of S and dP gives more
 // (8 x 4096 tokens, 12 heads on 4: 412 us, with K and V in their place 455), at d = 128 there is no room (with K
 // there and one dP tile a step takes 1920 cycles, with two dP tiles 1640).
-// 16384 tokens, 16 heads on 4: query side 1.19 ms at d = 128 and 0.88 at d = 64, key side 1.69 and 1.02 ms.
+// A CTA's start and end cost some 5 us (setting up, the first loads, a chain of products and elements with nothing
+// beside it, the results), a quarter of its time at 4096 tokens; CTAs that take one tile after another
+// instead of being launched anew were no faster.
+// 16384 tokens, 16 heads on 4: query side 1.17 ms at d = 128 and 0.83 at d = 64, key side 1.63 and 1.00 ms.
 //   warps 0-7, 8-15  element by element, the even and the odd steps: a thread has a row, 32 columns
 //   warps 16-18      issue the products (key side: 16-19; one product a warp, since its waits and commits
 //                    take longer than the product)
