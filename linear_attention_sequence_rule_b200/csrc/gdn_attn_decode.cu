@@ -81,11 +81,13 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// Tiles of a context (its length may be close to 2^31)
+__device__ __forceinline__ int context_tiles(int len) { return len > 0 ? (len - 1) / TT + 1 : 0; }
+
 // Tiles per split of a context of `len` tokens over at most `n` splits; those past its end are empty.
 __device__ __forceinline__ int split_tiles(int len, int n)
 {
-    const int tiles = len > 0 ? (len - 1) / TT + 1 : 0;
-    return max(1, (tiles + n - 1) / n);
+    return max(1, (context_tiles(len) + n - 1) / n);
 }
 
 __device__ __forceinline__ int context_len(const int32_t *lens, int n, int max_blocks, int page)
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(NW * 32, OCC)
     __syncwarp();
 
     const int shift = __ffs(a.page) - 1;
-    const int tiles = t1 > t0 ? (t1 - t0 - 1) / TT + 1 : 0;  // of this CTA; warp w takes tiles w, w + 4, ...
+    const int tiles = context_tiles(t1 - t0);           // of this CTA; warp w takes tiles w, w + 4, ...
     const int mine = tiles > warp ? (tiles - warp + NW - 1) / NW : 0;
     const int32_t *table = a.table + (int64_t)n * a.max_blocks;
     const bool small = a.page < TT;
@@ -530,8 +532,7 @@ __global__ void __launch_bounds__(JW * 32) attn_decode_join(const AttnDecodeArgs
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int len = context_len(a.lens, (int)(row / a.Hq), a.max_blocks, a.page);
-    const int tiles = (len + TT - 1) / TT, per = split_tiles(len, splits);
-    const int used = max(1, (tiles + per - 1) / per);
+    const int per = split_tiles(len, splits), used = max(1, (context_tiles(len) + per - 1) / per);
     const float *ws = static_cast<const float *>(a.workspace) + row * splits * (D + 4);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float M = -INFINITY;
