@@ -38,7 +38,7 @@ constexpr int TT = 32;    // tokens per tile
 constexpr int NW = 4;     // warps per CTA
 constexpr int NSTG = 2;   // ring stages per warp
 constexpr int OCC = 3;    // CTAs per SM: while one starts (a chain of dependent loads) the others stream (256 ragged
-                          // contexts: 379 us; with two CTAs of three stages 396)
+                          // contexts in order of number: 379 us; with two CTAs of three stages 396)
 constexpr int JW = 16;    // warps of the join
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -95,6 +95,75 @@ __device__ __forceinline__ int context_len(const int32_t *lens, int n, int max_b
     return (int)max(0LL, min((long long)lens[n], (long long)max_blocks * page));
 }
 
+// Requests in order of their lengths, the longest first, so that a launch of more CTAs than there are places does
+// not end with a long context alone: the request of a rank, found by every CTA for itself from all lengths
+// (at most kOrdered), in classes a quarter of a power of two wide and by number within a class.  It costs a
+// CTA about a microsecond, so contexts that cannot be long stay in order of number (256 contexts, 8 key heads, d 128,
+// of 128 to 8192 tokens: 334 us by length, 378 by number, 323 at the copy rate; to 2000: 112 and 118; to 300: 51 and 47).
+constexpr int kOrdered = 512, kOrderedFrom = 1024;  // requests, tokens
+__device__ __forceinline__ int request_of_rank(const int32_t *lens, int N, int max_blocks, int page, int rank)
+{
+    constexpr int NR = kOrdered / (NW * 32), CL = 128;
+    static_assert(CL == NW * 32 && NR * NW <= 32, "a class a thread, four a lane; a count a lane");
+    __shared__ __align__(16) int s_count[CL];
+    __shared__ int s_here[32], s_request;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int len[NR], cl[NR];
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        const int i = tid + NW * 32 * j;
+        len[j] = i < N ? context_len(lens, i, max_blocks, page) : -1;
+    }
+    s_count[tid] = 0;
+    if (tid < 32) s_here[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {  // the float's exponent and two bits of its fraction; class 0 are the longest
+        cl[j] = len[j] < 0 ? -1 : CL - 1 - (len[j] ? (int)(__float_as_uint((float)len[j]) >> 21) - (127 << 2) : 0);
+        if (cl[j] >= 0) atomicAdd(&s_count[cl[j]], 1);
+    }
+    __syncthreads();
+    // every warp: the class of this rank, and the rank within it
+    auto scan = [&](int x) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    };
+    const int4 c = reinterpret_cast<const int4 *>(s_count)[lane];
+    const int sum = c.x + c.y + c.z + c.w;
+    int k = rank - (scan(sum) - sum);  // within the lane's four classes
+    const int src = __ffs(__ballot_sync(0xffffffffu, k >= 0 && k < sum)) - 1;
+    int want = 4 * lane;
+    if (k >= c.x) {
+        k -= c.x, ++want;
+        if (k >= c.y) {
+            k -= c.y, ++want;
+            if (k >= c.z) k -= c.z, ++want;
+        }
+    }
+    want = __shfl_sync(0xffffffffu, want, src);
+    k = __shfl_sync(0xffffffffu, k, src);
+    // the k-th request of the class
+    unsigned in[NR];
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        in[j] = __ballot_sync(0xffffffffu, cl[j] == want);
+        if (lane == 0) s_here[NW * j + warp] = __popc(in[j]);
+    }
+    __syncthreads();
+    const int here = s_here[lane], before = scan(here) - here;
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        const int at = __shfl_sync(0xffffffffu, before, NW * j + warp) + __popc(in[j] & ((1u << lane) - 1));
+        if ((in[j] >> lane & 1) && at == k) s_request = tid + NW * 32 * j;
+    }
+    __syncthreads();
+    return s_request;
+}
+
 // Partial results lie in the workspace as [request x query head][split][d + 4]: o, then m and l of the
 // frame above (two floats unused).
 
@@ -125,7 +194,7 @@ template <int D> __host__ __device__ constexpr int decode_smem()
 template <int D, bool F32>
 __global__ void __launch_bounds__(NW * 32, OCC)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                       const AttnDecodeArgs a, int splits, int mtiles)
+                       const AttnDecodeArgs a, int splits, int mtiles, int ordered)
 {
     constexpr int MH = F32 ? 8 : 16;  // heads per tile
     constexpr int KS = D / 16;        // k steps of the score product
@@ -144,7 +213,8 @@ __global__ void __launch_bounds__(NW * 32, OCC)
     idx /= splits;
     const int mt = idx % mtiles;
     idx /= mtiles;
-    const int hk = idx % a.Hk, n = idx / a.Hk;
+    const int hk = idx % a.Hk;
+    const int n = ordered ? request_of_rank(a.lens, a.N, a.max_blocks, a.page, idx / a.Hk) : idx / a.Hk;
     const int G = a.Hq / a.Hk;
     const int len = context_len(a.lens, n, a.max_blocks, a.page);
     const int per = split_tiles(len, splits);
@@ -585,16 +655,17 @@ int head_tiles(int G, int dtype) { return (G + (dtype == GDN_DTYPE_F32 ? 8 : 16)
 // - few (request, key head) pairs: one CTA for each place on the SMs, down to a tile a warp (one context of
 //   65536 tokens, 4 key heads: 22.8 us in 64 or 111 splits, 31 in 32, 27 in 255; of 4096: 7.9 us in 32
 //   splits, 8.9 in 16);
-// - more: about 2.3 for each place, so that the longest contexts of a ragged batch do not end the launch
-//   alone, down to two tiles a warp (contexts of 128 to 8192 tokens, 8 key heads: 16 of them 43 us in 8
-//   splits, 63 in 2; 256 of them 379 unsplit, 403 in 2).
+// - more: about 1.5 for each place, down to two tiles a warp (contexts of 128 to 8192 tokens, 8 key heads: 16 of
+//   them 40.6 us in 6 splits, 43.8 in 8, 43.0 in 4; 48 of them 79.6 in 2, 87.0 in 3);
+// - pairs for all places: two splits only where they leave 16 tiles a warp (64 contexts of 128 to 8192 tokens, 8
+//   key heads: 120 us in 2, 127 in 1; of 128 to 2000: 53 and 41).
 int split_count(int N, int Hk, int mtiles, int page, int max_blocks)
 {
     const long tiles = ((long)max_blocks * page + TT - 1) / TT;
     const long units = (long)N * Hk * mtiles, places = (long)OCC * sm_count();
     const bool few = units * 16 <= places;
-    const long s = few ? places / units : (23 * places / 10 + units - 1) / units;
-    const long most = few ? tiles / NW : tiles / (2 * NW);
+    const long s = few ? places / units : (3 * places / 2 + units - 1) / units;
+    const long most = few ? tiles / NW : tiles / ((units < places ? 2 : 16) * NW);
     return (int)(s > most ? (most < 1 ? 1 : most) : (s < 1 ? 1 : s));
 }
 
@@ -622,7 +693,9 @@ template <int D, bool F32> cudaError_t run_decode(const AttnDecodeArgs &a, cudaS
     auto kern = attn_decode_kernel<D, F32>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long)a.N * a.Hk * mtiles * splits), NW * 32, smem, st>>>(mk, mv, a, splits, mtiles);
+    const long ctas = (long)a.N * a.Hk * mtiles * splits;
+    const int ordered = a.N > 1 && a.N <= kOrdered && (long)a.max_blocks * a.page >= kOrderedFrom && ctas > (long)OCC * sm_count();
+    kern<<<(unsigned)ctas, NW * 32, smem, st>>>(mk, mv, a, splits, mtiles, ordered);
     e = cudaGetLastError();
     if (e != cudaSuccess || splits == 1) return e;
     // the join's CTAs may be set up while the last ones above run; they wait for all of them

@@ -341,6 +341,24 @@ def test_decode_many_requests_some_long(page, dtype):
     decode_both(q, kc, vc, ks, vs, table, lens, dtype, scale=0.02)
 
 
+@pytest.mark.parametrize("lens", ["any", "equal", "empty", "one", "classes"])
+@pytest.mark.parametrize("n", [2, 31, 129, 512, 513])
+def test_decode_order_of_the_requests(n, lens):
+    """More CTAs than places: every request is worked on once, in whatever order its length gives."""
+    page, d, Hk = 64, 64, 8 if n > 31 else 40
+    r = np.random.RandomState(n)
+    lengths = dict(any=r.randint(0, 1100, n), equal=np.full(n, 70), empty=np.zeros(n, int), one=np.ones(n, int),
+                   classes=2 ** r.randint(0, 11, n) + r.randint(-1, 2, n))[lens].copy()
+    if lens == "any":
+        lengths[[0, n - 1]] = -3, 1100
+    table, _ = table_of(np.maximum(lengths, 0), page, 18, seed=60)
+    P = max(int(table.max()) + 1, 1)
+    kc, ks = filled_cache(P, Hk, page, d, 61)
+    vc, vs = filled_cache(P, Hk, page, d, 62)
+    q = torch.randn(n, Hk, d, generator=torch.Generator().manual_seed(63)).bfloat16()
+    decode_both(q, kc, vc, ks, vs, table, lengths, "bf16", scale=0.02)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_decode_heads_do_not_touch_one_another(dtype):
     """A head's result does not depend on what the heads beside it hold: huge, tiny, infinite or NaN."""
