@@ -4,10 +4,12 @@
 // Per (request, key head): s_j = scale q . (ks_j K8_j), out = sum_j softmax_j(s) vs_j V8_j over the
 // request's cached tokens, for the G query heads that share the key head.  HBM bounds it: 2 d bytes
 // per token and key head against 4 G d flops.  The cache is therefore read once for up to 16 query
-// heads: they are the M = 16 rows of warp-level MMAs (m16n8k16, fp16 operands, fp32 accumulators)
-// whose B operands are the cached bytes, converted to fp16 (exact) in registers.  At 2 d bytes per
-// token these MMAs leave the tensor pipe mostly idle, so the 128-row tcgen05 shape, which would pad
-// G rows to 128 and need the bytes converted through shared memory, has nothing to give here.
+// heads by warp-level MMAs (m16n8k16, fp16 operands, fp32 accumulators): the cached bytes, converted to fp16
+// (exact) in registers, are their A operands (16 tokens of K; 16 elements of V, transposed), and 8 heads their N
+// columns, so that few heads leave little idle: conversions are made once for all heads, and with up to 8 of them
+// half the MMAs and exponentials of a layout with heads as rows do (256 contexts of up to 8192 tokens, 4 heads on
+// one: TODO).  The 128-row tcgen05 shape, which would pad G rows to 128 and need the bytes converted through shared
+// memory, has nothing to give here.
 //
 // Each warp runs alone: it takes every fourth 32-token tile of its CTA's range through its own ring
 // of TMA loads (K and V tiles of 32 rows, swizzled), keeps its own running maximum, sum and output
@@ -190,15 +192,29 @@ template <int D> __host__ __device__ constexpr int decode_smem()
     return 1024 + ring_bytes<D>() + NW * NSTG * ((int)sizeof(TileInfo) + 8) + NW * 16 * 8;
 }
 
-// F32: q as a sum of two fp16 in rows g and g + 8 (8 heads per tile), the weights likewise.
-template <int D, bool F32>
+// bf16 calls in groups of 8 heads or, with more than 8 on a key head, of 16; fp32 calls in groups of 8, q and the weights
+// as sums of two fp16.
+enum { kHeads8, kHeads16, kFloat };
+
+// 8 x 8 of 16 bits, transposed: thread (g, c) gives row g, columns 2c and 2c + 1, and gets column g, rows 2c and 2c + 1
+__device__ __forceinline__ uint32_t transposed(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+template <int D, int KIND>
 __global__ void __launch_bounds__(NW * 32, OCC)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const AttnDecodeArgs a, int splits, int mtiles, int ordered)
 {
-    constexpr int MH = F32 ? 8 : 16;  // heads per tile
+    constexpr bool F32 = KIND == kFloat;
+    constexpr int NA = KIND == kHeads16 ? 2 : 1;  // groups of 8 heads
+    constexpr int NQ = KIND == kHeads8 ? 1 : 2;   // B operands of q: the groups, or q's two parts
+    constexpr int MH = 8 * NA;                    // heads of a CTA
     constexpr int KS = D / 16;        // k steps of the score product
-    constexpr int ND = D / 8;         // column tiles of the value product
+    constexpr int ND = D / 16;        // row tiles of the value product
     constexpr int NG = D / 32;        // 4-byte words of a V row per thread
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -302,13 +318,13 @@ __global__ void __launch_bounds__(NW * 32, OCC)
     for (int i = 0; i < issued; ++i) note(i);
     __syncwarp();
 
-    // ---- q as A fragments; thread (g, c) holds rows g and g + 8 and, at k step ks, the four d values
-    // of its 16-byte chunks of a K row: chunk 2c + i (D = 128) or c (D = 64), word e, ks = 4 i + e ----
-    uint32_t qa[KS][4];
-    float unscale0, unscale1;  // score = accumulated x unscale x ks, rows g and g + 8
+    // ---- q as B operands; thread (g, c) holds heads g and g + 8 and, at k step ks, the four d values of its 16-byte
+    // chunks of a K row: chunk 2c + i (D = 128) or c (D = 64), word e, ks = 4 i + e ----
+    uint32_t qb[NQ][KS][2];
+    float unscale[NA][2];  // score = accumulated x unscale x ks, heads 2c and 2c + 1 of a group
     {
         const int h0 = mt * MH + g, h1 = F32 ? h0 : h0 + 8;
-        const bool on0 = h0 < G, on1 = h1 < G;
+        const bool on0 = h0 < G, on1 = KIND == kHeads16 && h1 < G;
         const int64_t r0 = ((int64_t)n * a.Hq + hk * G + h0) * D, r1 = ((int64_t)n * a.Hq + hk * G + h1) * D;
         float x0[KS][4], x1[KS][4];
         float mx0 = 0.f, mx1 = 0.f;
@@ -355,8 +371,11 @@ __global__ void __launch_bounds__(NW * 32, OCC)
         auto two_to = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
         const int e0 = exponent(mx0), e1 = exponent(mx1);
         const float down0 = two_to(-e0), down1 = two_to(-e1);
-        unscale0 = two_to(e0) * a.scale * kLog2e;
-        unscale1 = two_to(e1) * a.scale * kLog2e;
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)  // thread (h, 0) knows head h's
+                unscale[i][e] = two_to(__shfl_sync(0xffffffffu, i ? e1 : e0, 4 * (2 * c + e))) * a.scale * kLog2e;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
@@ -364,23 +383,30 @@ __global__ void __launch_bounds__(NW * 32, OCC)
                 x0[ks][j] *= down0;
                 x1[ks][j] *= down1;
             }
-            if (F32) {  // row g + 8: what fp16 rounding of row g left over
+            if (F32) {  // the second part: what fp16 rounding left over
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x1[ks][j] = x0[ks][j] - __half2float(__float2half_rn(x0[ks][j]));
             }
-            qa[ks][0] = pack_half(x0[ks][0], x0[ks][1]);
-            qa[ks][1] = pack_half(x1[ks][0], x1[ks][1]);
-            qa[ks][2] = pack_half(x0[ks][2], x0[ks][3]);
-            qa[ks][3] = pack_half(x1[ks][2], x1[ks][3]);
+            qb[0][ks][0] = pack_half(x0[ks][0], x0[ks][1]);
+            qb[0][ks][1] = pack_half(x0[ks][2], x0[ks][3]);
+            if (NQ == 2) {
+                qb[NQ - 1][ks][0] = pack_half(x1[ks][0], x1[ks][1]);
+                qb[NQ - 1][ks][1] = pack_half(x1[ks][2], x1[ks][3]);
+            }
         }
     }
 
-    float o[ND][4];
+    // o[i][4 rows of V^T, 2 heads]: tile 2x + t, register 2u + e: d = 4 (g + 8 x) + 2 t + u, head 2c + e of group i
+    float o[NA][ND][4], m[NA][2], l[NA][2];
 #pragma unroll
-    for (int i = 0; i < ND; ++i)
+    for (int i = 0; i < NA; ++i) {
+        m[i][0] = m[i][1] = -INFINITY;
+        l[i][0] = l[i][1] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        for (int x = 0; x < ND; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][x][j] = 0.f;
+    }
     // D = 64: a thread with odd c reads its token pairs in the other order (bank conflicts, below)
     const uint32_t sel_lo = (D == 64 && (c & 1)) ? 0x1504u : 0x5140u, sel_hi = (D == 64 && (c & 1)) ? 0x3726u : 0x7362u;
     const int odd = D == 64 ? (c & 1) : 0;
@@ -408,91 +434,93 @@ __global__ void __launch_bounds__(NW * 32, OCC)
                     for (int w = lane; w < D / 4; w += 32) reinterpret_cast<uint32_t *>(vt + r * D)[w] = 0u;
             __syncwarp();
         }
-        // ---- scores: 16 rows x 32 tokens ----
-        float s[4][4];
+        // ---- scores: 2 x 16 tokens x 8 heads: register 2u + e of tile t is token 16 t + 8 u + g, head 2c + e ----
+        float s[NA][2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int t = 0; t < 2; ++t) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-            const int row = 8 * j + g;
+            for (int x = 0; x < NA; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[x][t][e] = 0.f;
+            const int row = 16 * t + g;
 #pragma unroll
             for (int i2 = 0; i2 < D / 64; ++i2) {
                 // the swizzle XORs the 16-byte chunk with the row (D = 128) or row pair (D = 64):
                 // the eight threads of a phase then read eight different chunk columns
                 const int ch = D == 128 ? ((2 * c + i2) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
                 const uint4 w = *reinterpret_cast<const uint4 *>(kt + row * D + ch * 16);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                const uint4 y = *reinterpret_cast<const uint4 *>(kt + (row + 8) * D + ch * 16);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w}, yy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int ks = 4 * i2 + e;
-                    mma_f16(s[j], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], cvt_lo(ww[e]), cvt_hi(ww[e]));
+                    const uint32_t a0 = cvt_lo(ww[e]), a1 = cvt_lo(yy[e]), a2 = cvt_hi(ww[e]), a3 = cvt_hi(yy[e]);
+#pragma unroll
+                    for (int x = 0; x < NQ; ++x) mma_f16(s[x % NA][t], a0, a1, a2, a3, qb[x][ks][0], qb[x][ks][1]);
                 }
             }
         }
         // ---- softmax weights ----
-        const float fA = unscale0 * kA, fB = unscale0 * ksB, hA = unscale1 * kA, hB = unscale1 * ksB;
         const float lgA = onA ? log2f(vA) : 0.f, lgB = onB ? log2f(vsB) : 0.f;
-        float mx0 = -INFINITY, mx1 = -INFINITY;
+        float mx[NA][2];
+        bool up = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float f = j < 2 ? fA : fB, h = j < 2 ? hA : hB, lg = j < 2 ? lgA : lgB;
-            const bool onj = j < 2 ? onA : onB;
+        for (int x = 0; x < NA; ++x)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const bool on = onj && 8 * j + 2 * c + e < live;
-                if (F32) {
-                    const float x = s[j][e] + s[j][e + 2];
-                    s[j][e] = on ? fmaf(x, f, lg) : -INFINITY;
-                } else {
-                    s[j][e] = on ? fmaf(s[j][e], f, lg) : -INFINITY;
-                    s[j][e + 2] = on ? fmaf(s[j][e + 2], h, lg) : -INFINITY;
-                    mx1 = fmaxf(mx1, s[j][e + 2]);
-                }
-                mx0 = fmaxf(mx0, s[j][e]);
-            }
-        }
+                const float fA = unscale[x][e] * kA, fB = unscale[x][e] * ksB;
+                mx[x][e] = -INFINITY;
 #pragma unroll
-        for (int x = 1; x < 4; x <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
-            if (!F32) mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
-        }
-        const bool up = mx0 > m0 || (!F32 && mx1 > m1);
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const bool on = (t ? onB : onA) && 16 * t + 8 * u + g < live;
+                        float &y = s[x][t][2 * u + e];
+                        y = on ? fmaf(y, t ? fB : fA, t ? lgB : lgA) : -INFINITY;
+                        mx[x][e] = fmaxf(mx[x][e], y);
+                    }
+#pragma unroll
+                for (int b = 4; b < 32; b <<= 1) mx[x][e] = fmaxf(mx[x][e], __shfl_xor_sync(0xffffffffu, mx[x][e], b));
+                up |= mx[x][e] > m[x][e];
+            }
         if (__any_sync(0xffffffffu, up)) {
-            const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-            const float f0 = n0 == -INFINITY ? 1.f : ex2_approx(m0 - n0);
-            const float f1 = F32 ? f0 : (n1 == -INFINITY ? 1.f : ex2_approx(m1 - n1));
-            m0 = n0;
-            m1 = n1;
-            l0 *= f0;
-            l1 *= f1;
 #pragma unroll
-            for (int x = 0; x < ND; ++x) {
-                o[x][0] *= f0;
-                o[x][1] *= f0;
-                o[x][2] *= f1;
-                o[x][3] *= f1;
-            }
+            for (int x = 0; x < NA; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float to = fmaxf(m[x][e], mx[x][e]);
+                    const float f = to == -INFINITY ? 1.f : ex2_approx(m[x][e] - to);
+                    m[x][e] = to;
+                    l[x][e] *= f;
+#pragma unroll
+                    for (int i3 = 0; i3 < ND; ++i3) {
+                        o[x][i3][e] *= f;
+                        o[x][i3][2 + e] *= f;
+                    }
+                }
         }
-        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
         const float iA = onA ? 1.f / vA : 0.f, iB = onB ? 1.f / vsB : 0.f;
-        uint32_t pa[4][2];  // per 8-token column tile: rows g, g + 8
+        uint32_t pb[NQ][2][2];  // weights as B operands of 16 tokens: the groups, or the weights' two parts
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float iv = j < 2 ? iA : iB;
-            const float x0 = ex2_approx(s[j][0] - b0), x1 = ex2_approx(s[j][1] - b0);
-            l0 = fmaf(x0 + x1, iv, l0);
-            pa[j][0] = pack_half(x0, x1);
-            if (F32) {
-                const __half2 hi = *reinterpret_cast<const __half2 *>(&pa[j][0]);
-                pa[j][1] = pack_half(x0 - __low2float(hi), x1 - __high2float(hi));
-            } else {
-                const float y0 = ex2_approx(s[j][2] - b1), y1 = ex2_approx(s[j][3] - b1);
-                l1 = fmaf(y0 + y1, iv, l1);
-                pa[j][1] = pack_half(y0, y1);
-            }
+        for (int x = 0; x < NA; ++x) {
+            const float b0 = m[x][0] == -INFINITY ? 0.f : m[x][0], b1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float y0 = ex2_approx(s[x][t][2 * u] - b0), y1 = ex2_approx(s[x][t][2 * u + 1] - b1);
+                    l[x][0] = fmaf(y0, t ? iB : iA, l[x][0]);
+                    l[x][1] = fmaf(y1, t ? iB : iA, l[x][1]);
+                    const uint32_t w = pack_half(y0, y1);
+                    pb[x][t][u] = transposed(w);
+                    if (F32) {
+                        const __half2 hi = *reinterpret_cast<const __half2 *>(&w);
+                        pb[NQ - 1][t][u] = transposed(pack_half(y0 - __low2float(hi), y1 - __high2float(hi)));
+                    }
+                }
         }
-        // ---- o += p V: k = 16 tokens a step; thread (g, c) reads words g + 8 x of the rows 2c, 2c + 1,
-        // 2c + 8, 2c + 9, column tile 4 x + b <-> d = 4 (g + 8 x) + b ----
+        // ---- o += V^T p: k = 16 tokens a step; thread (g, c) reads words g + 8 x of the rows 2c, 2c + 1,
+        // 2c + 8, 2c + 9; bytes 2 t and 2 t + 1 of a word are rows g and g + 8 of tile 2 x + t ----
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
 #pragma unroll
@@ -510,11 +538,13 @@ __global__ void __launch_bounds__(NW * 32, OCC)
                 // bytes of two tokens side by side: (token 2c, token 2c + 1) of each d
                 const uint32_t u0 = __byte_perm(w[0], w[1], sel_lo), u1 = __byte_perm(w[0], w[1], sel_hi);
                 const uint32_t z0 = __byte_perm(w[2], w[3], sel_lo), z1 = __byte_perm(w[2], w[3], sel_hi);
-                const uint32_t A0 = pa[2 * k2][0], A1 = pa[2 * k2][1], A2 = pa[2 * k2 + 1][0], A3 = pa[2 * k2 + 1][1];
-                mma_f16(o[4 * x + 0], A0, A1, A2, A3, cvt_lo(u0), cvt_lo(z0));
-                mma_f16(o[4 * x + 1], A0, A1, A2, A3, cvt_hi(u0), cvt_hi(z0));
-                mma_f16(o[4 * x + 2], A0, A1, A2, A3, cvt_lo(u1), cvt_lo(z1));
-                mma_f16(o[4 * x + 3], A0, A1, A2, A3, cvt_hi(u1), cvt_hi(z1));
+                const uint32_t a0 = cvt_lo(u0), a1 = cvt_hi(u0), a2 = cvt_lo(z0), a3 = cvt_hi(z0);
+                const uint32_t c0 = cvt_lo(u1), c1 = cvt_hi(u1), c2 = cvt_lo(z1), c3 = cvt_hi(z1);
+#pragma unroll
+                for (int y = 0; y < NQ; ++y) {
+                    mma_f16(o[y % NA][2 * x], a0, a1, a2, a3, pb[y][k2][0], pb[y][k2][1]);
+                    mma_f16(o[y % NA][2 * x + 1], c0, c1, c2, c3, pb[y][k2][0], pb[y][k2][1]);
+                }
             }
         }
         if (partial) fence_proxy_async_smem();  // the zeros, before the stage's next bytes
@@ -530,35 +560,24 @@ __global__ void __launch_bounds__(NW * 32, OCC)
 
     // ---- the four warps join through shared memory (their rings are free now) ----
 #pragma unroll
-    for (int x = 1; x < 4; x <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-    }
-    if (F32) {
+    for (int i = 0; i < NA; ++i)
 #pragma unroll
-        for (int x = 0; x < ND; ++x) {
-            o[x][0] += o[x][2];
-            o[x][1] += o[x][3];
-        }
-    }
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], x);
     __syncthreads();
     float *so = reinterpret_cast<float *>(sm) + warp * MH * D;
-    if (c == 0) {
-        s_ml[warp * 16 + g] = make_float2(m0, l0);
-        if (!F32) s_ml[warp * 16 + g + 8] = make_float2(m1, l1);
-    }
 #pragma unroll
-    for (int x = 0; x < NG; ++x) {
-        const int d0 = 4 * (2 * c + 8 * x);
+    for (int i = 0; i < NA; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            *reinterpret_cast<float4 *>(so + g * D + d0 + 4 * e) =
-                make_float4(o[4 * x][e], o[4 * x + 1][e], o[4 * x + 2][e], o[4 * x + 3][e]);
-            if (!F32)
-                *reinterpret_cast<float4 *>(so + (g + 8) * D + d0 + 4 * e) =
-                    make_float4(o[4 * x][2 + e], o[4 * x + 1][2 + e], o[4 * x + 2][2 + e], o[4 * x + 3][2 + e]);
+            const int r = 8 * i + 2 * c + e;
+            if (g == 0) s_ml[warp * 16 + r] = make_float2(m[i][e], l[i][e]);
+#pragma unroll
+            for (int x = 0; x < NG; ++x)
+                *reinterpret_cast<float4 *>(so + r * D + 4 * (g + 8 * x)) =
+                    make_float4(o[i][2 * x][e], o[i][2 * x][2 + e], o[i][2 * x + 1][e], o[i][2 * x + 1][2 + e]);
         }
-    }
     __syncthreads();
     const float *all = reinterpret_cast<const float *>(sm);
     for (int i = tid; i < MH * (D / 4); i += NW * 32) {
@@ -649,7 +668,12 @@ int sm_count()
     return n;
 }
 
-int head_tiles(int G, int dtype) { return (G + (dtype == GDN_DTYPE_F32 ? 8 : 16) - 1) / (dtype == GDN_DTYPE_F32 ? 8 : 16); }
+int kind_of(int G, int dtype) { return dtype == GDN_DTYPE_F32 ? kFloat : G > 8 ? kHeads16 : kHeads8; }
+int head_tiles(int G, int dtype)
+{
+    const int mh = kind_of(G, dtype) == kHeads16 ? 16 : 8;
+    return (G + mh - 1) / mh;
+}
 
 // Splits of a context.  A CTA starts with a chain of dependent loads, some 5 us, so splits beyond need cost:
 // - few (request, key head) pairs: one CTA for each place on the SMs, down to a tile a warp (one context of
@@ -682,7 +706,7 @@ bool cache_map(CUtensorMap *m, const void *base, int num_pages, int Hk, int page
                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool F32> cudaError_t run_decode(const AttnDecodeArgs &a, cudaStream_t st)
+template <int D, int KIND> cudaError_t run_decode(const AttnDecodeArgs &a, cudaStream_t st)
 {
     CUtensorMap mk, mv;
     if (!cache_map(&mk, a.k_cache, a.num_pages, a.Hk, a.page, D) || !cache_map(&mv, a.v_cache, a.num_pages, a.Hk, a.page, D))
@@ -690,7 +714,7 @@ template <int D, bool F32> cudaError_t run_decode(const AttnDecodeArgs &a, cudaS
     const int mtiles = head_tiles(a.Hq / a.Hk, a.dtype);
     const int splits = split_count(a.N, a.Hk, mtiles, a.page, a.max_blocks);
     constexpr int smem = decode_smem<D>();
-    auto kern = attn_decode_kernel<D, F32>;
+    auto kern = attn_decode_kernel<D, KIND>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const long ctas = (long)a.N * a.Hk * mtiles * splits;
@@ -708,7 +732,7 @@ template <int D, bool F32> cudaError_t run_decode(const AttnDecodeArgs &a, cudaS
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_decode_join<D, F32>, a, splits);
+    return cudaLaunchKernelEx(&cfg, attn_decode_join<D, KIND == kFloat>, a, splits);
 }
 
 }  // namespace
@@ -721,8 +745,11 @@ size_t attn_decode_workspace_bytes(int N, int Hq, int Hk, int d, int page, int m
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t st)
 {
-    if (a.dtype == GDN_DTYPE_F32) return a.d == 128 ? run_decode<128, true>(a, st) : run_decode<64, true>(a, st);
-    return a.d == 128 ? run_decode<128, false>(a, st) : run_decode<64, false>(a, st);
+    switch (kind_of(a.Hq / a.Hk, a.dtype)) {
+        case kHeads8: return a.d == 128 ? run_decode<128, kHeads8>(a, st) : run_decode<64, kHeads8>(a, st);
+        case kHeads16: return a.d == 128 ? run_decode<128, kHeads16>(a, st) : run_decode<64, kHeads16>(a, st);
+        default: return a.d == 128 ? run_decode<128, kFloat>(a, st) : run_decode<64, kFloat>(a, st);
+    }
 }
 
 int read_and_clear_attn_decode_error()
