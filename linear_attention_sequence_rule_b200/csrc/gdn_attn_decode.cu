@@ -8,7 +8,7 @@
 // (exact) in registers, are their A operands (16 tokens of K; 16 elements of V, transposed), and 8 heads their N
 // columns, so that few heads leave little idle: conversions are made once for all heads, and with up to 8 of them
 // half the MMAs and exponentials of a layout with heads as rows do (256 contexts of up to 8192 tokens, 4 heads on
-// one: TODO).  The 128-row tcgen05 shape, which would pad G rows to 128 and need the bytes converted through shared
+// one: 301 us, with heads as rows 334).  The 128-row tcgen05 shape, which would pad G rows to 128 and need the bytes converted through shared
 // memory, has nothing to give here.
 //
 // Each warp runs alone: it takes every fourth 32-token tile of its CTA's range through its own ring
@@ -40,7 +40,7 @@ constexpr int TT = 32;    // tokens per tile
 constexpr int NW = 4;     // warps per CTA
 constexpr int NSTG = 2;   // ring stages per warp
 constexpr int OCC = 3;    // CTAs per SM: while one starts (a chain of dependent loads) the others stream (256 ragged
-                          // contexts in order of number: 379 us; with two CTAs of three stages 396)
+                          // contexts: 301 us; with two CTAs of three stages 319)
 constexpr int JW = 16;    // warps of the join
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -100,9 +100,9 @@ __device__ __forceinline__ int context_len(const int32_t *lens, int n, int max_b
 // Requests in order of their lengths, the longest first, so that a launch of more CTAs than there are places does
 // not end with a long context alone: the request of a rank, found by every CTA for itself from all lengths
 // (at most kOrdered), in classes a quarter of a power of two wide and by number within a class.  It costs a
-// CTA about a microsecond, so contexts that cannot be long stay in order of number (256 contexts, 8 key heads, d 128,
-// of 128 to 8192 tokens: 334 us by length, 378 by number, 323 at the copy rate; to 2000: 112 and 118; to 300: 51 and 47).
-constexpr int kOrdered = 512, kOrderedFrom = 1024;  // requests, tokens
+// CTA about a microsecond, so contexts that cannot be long stay in order of number (8 key heads, d 128: 256 contexts of
+// 128 to 8192 tokens 301 us by length, 324 by number; 64 of up to 2000 33 and 38; 256 of up to 1000 67 and 61).
+constexpr int kOrdered = 512, kOrderedFrom = 2048;  // requests, tokens
 __device__ __forceinline__ int request_of_rank(const int32_t *lens, int N, int max_blocks, int page, int rank)
 {
     constexpr int NR = kOrdered / (NW * 32), CL = 128;
@@ -677,12 +677,12 @@ int head_tiles(int G, int dtype)
 
 // Splits of a context.  A CTA starts with a chain of dependent loads, some 5 us, so splits beyond need cost:
 // - few (request, key head) pairs: one CTA for each place on the SMs, down to a tile a warp (one context of
-//   65536 tokens, 4 key heads: 22.8 us in 64 or 111 splits, 31 in 32, 27 in 255; of 4096: 7.9 us in 32
-//   splits, 8.9 in 16);
+//   65536 tokens, 4 key heads: 19.3 us in 111 splits, 20.4 in 55, 26 in 27, 25 in 222; of 4096: 7.2 us in 32
+//   splits, 8.2 in 27);
 // - more: about 1.5 for each place, down to two tiles a warp (contexts of 128 to 8192 tokens, 8 key heads: 16 of
-//   them 40.6 us in 6 splits, 43.8 in 8, 43.0 in 4; 48 of them 79.6 in 2, 87.0 in 3);
+//   them 34.7 us in 6 splits, 37.9 in 8, 34.8 in 4; 32 of them 56.4 in 3, 59.7 in 4, 57.9 in 2);
 // - pairs for all places: two splits only where they leave 16 tiles a warp (64 contexts of 128 to 8192 tokens, 8
-//   key heads: 120 us in 2, 127 in 1; of 128 to 2000: 53 and 41).
+//   key heads: 109 us in 2, 103 in 1; of up to 32768: 306 and 357; of up to 2000: 47 and 33).
 int split_count(int N, int Hk, int mtiles, int page, int max_blocks)
 {
     const long tiles = ((long)max_blocks * page + TT - 1) / TT;
