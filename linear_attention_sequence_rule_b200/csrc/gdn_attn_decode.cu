@@ -180,10 +180,10 @@ template <bool F32> __device__ __forceinline__ void store_out(void *out, int64_t
 
 template <int D> __host__ __device__ constexpr int stage_bytes() { return 2 * TT * D; }
 template <int D> __host__ __device__ constexpr int ring_bytes() { return NW * NSTG * stage_bytes<D>(); }
-// What a stage's tile needs besides its bytes: its pages' scales; a scale below 0 marks tokens that
-// are left out.
-struct TileInfo {
-    float ks0, ks1, vs0, vs1;  // tokens 0-15 and 16-31 of the tile
+// What a stage's tile needs besides its bytes, for its tokens 0-15 and 16-31: its pages' key scale, log2 and
+// reciprocal of the value scale; one below 0 marks tokens that are left out.
+struct alignas(32) TileInfo {
+    float ks0, ks1, lg0, lg1, iv0, iv1;
 };
 
 // behind the ring: the stages' info, barriers, then the warps' (m, l) for the join
@@ -255,7 +255,11 @@ __global__ void __launch_bounds__(NW * 32, OCC)
     // tokens), with the next 32 fetched while these are worked on, so that the chain table -> scale
     // is waited for once.
     int pg0, pg1, npg0 = -1, npg1 = -1;
-    float ks0, ks1, vs0, vs1, nks0 = 0.f, nks1 = 0.f, nvs0 = 0.f, nvs1 = 0.f;
+    float nks0 = 0.f, nks1 = 0.f, nvs0 = 0.f, nvs1 = 0.f;
+    TileInfo own;
+    auto take_scales = [&]() {
+        own = TileInfo{nks0, nks1, log2f(nvs0), log2f(nvs1), 1.f / nvs0, 1.f / nvs1};
+    };
     auto fetch_pages = [&](int i0, int &p0, int &p1) {
         p0 = p1 = -1;
         if (i0 + lane < mine) {
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(NW * 32, OCC)
         const int at = i & 31;
         if (at == 0 && i > 0) {
             pg0 = npg0, pg1 = npg1;
-            ks0 = nks0, ks1 = nks1, vs0 = nvs0, vs1 = nvs1;
+            take_scales();
         }
         const int p0 = max(__shfl_sync(0xffffffffu, pg0, at), 0), p1 = max(__shfl_sync(0xffffffffu, pg1, at), 0);
         if (lane == 0) {
@@ -307,14 +311,15 @@ __global__ void __launch_bounds__(NW * 32, OCC)
     // The scales of tile i, behind its loads: they come from memory as its bytes do.
     auto note = [&](int i) {
         const int at = i & 31;
-        if (lane == at) info[i % NSTG] = TileInfo{ks0, ks1, vs0, vs1};
+        if (lane == at) info[i % NSTG] = own;
         if (at == 8) fetch_pages(i - 8 + 32, npg0, npg1);
         if (at == 20) fetch_scales(npg0, npg1, nks0, nks1, nvs0, nvs1);
     };
     fetch_pages(0, pg0, pg1);
     int issued = 0;
     for (; issued < NSTG && issued < mine; ++issued) load(issued);
-    fetch_scales(pg0, pg1, ks0, ks1, vs0, vs1);
+    fetch_scales(pg0, pg1, nks0, nks1, nvs0, nvs1);
+    take_scales();
     for (int i = 0; i < issued; ++i) note(i);
     __syncwarp();
 
@@ -423,8 +428,8 @@ __global__ void __launch_bounds__(NW * 32, OCC)
         const int tok = t0 + (warp + NW * i) * TT;
         const int live = min(TT, t1 - tok);
         const TileInfo ti = info[i % NSTG];
-        const float kA = ti.ks0, ksB = ti.ks1, vA = ti.vs0, vsB = ti.vs1;
-        const bool onA = !(vA < 0.f), onB = !(vsB < 0.f);
+        const float iA = ti.iv0, iB = ti.iv1;
+        const bool onA = !(iA < 0.f), onB = !(iB < 0.f);
         // V rows that are not part of the context may hold any byte, NaN among them: zero them,
         // since a weight of 0 times NaN is NaN
         const bool partial = live < TT || !onA || !onB;
@@ -461,14 +466,14 @@ __global__ void __launch_bounds__(NW * 32, OCC)
             }
         }
         // ---- softmax weights ----
-        const float lgA = onA ? log2f(vA) : 0.f, lgB = onB ? log2f(vsB) : 0.f;
+        // (the lanes' maxima are joined only where one of them passes the running one)
         float mx[NA][2];
         bool up = false;
 #pragma unroll
         for (int x = 0; x < NA; ++x)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float fA = unscale[x][e] * kA, fB = unscale[x][e] * ksB;
+                const float fA = unscale[x][e] * ti.ks0, fB = unscale[x][e] * ti.ks1;
                 mx[x][e] = -INFINITY;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
@@ -476,11 +481,9 @@ __global__ void __launch_bounds__(NW * 32, OCC)
                     for (int u = 0; u < 2; ++u) {
                         const bool on = (t ? onB : onA) && 16 * t + 8 * u + g < live;
                         float &y = s[x][t][2 * u + e];
-                        y = on ? fmaf(y, t ? fB : fA, t ? lgB : lgA) : -INFINITY;
+                        y = on ? fmaf(y, t ? fB : fA, t ? ti.lg1 : ti.lg0) : -INFINITY;
                         mx[x][e] = fmaxf(mx[x][e], y);
                     }
-#pragma unroll
-                for (int b = 4; b < 32; b <<= 1) mx[x][e] = fmaxf(mx[x][e], __shfl_xor_sync(0xffffffffu, mx[x][e], b));
                 up |= mx[x][e] > m[x][e];
             }
         if (__any_sync(0xffffffffu, up)) {
@@ -488,6 +491,8 @@ __global__ void __launch_bounds__(NW * 32, OCC)
             for (int x = 0; x < NA; ++x)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int b = 4; b < 32; b <<= 1) mx[x][e] = fmaxf(mx[x][e], __shfl_xor_sync(0xffffffffu, mx[x][e], b));
                     const float to = fmaxf(m[x][e], mx[x][e]);
                     const float f = to == -INFINITY ? 1.f : ex2_approx(m[x][e] - to);
                     m[x][e] = to;
@@ -499,7 +504,6 @@ __global__ void __launch_bounds__(NW * 32, OCC)
                     }
                 }
         }
-        const float iA = onA ? 1.f / vA : 0.f, iB = onB ? 1.f / vsB : 0.f;
         uint32_t pb[NQ][2][2];  // weights as B operands of 16 tokens: the groups, or the weights' two parts
 #pragma unroll
         for (int x = 0; x < NA; ++x) {
