@@ -230,13 +230,17 @@ template <> struct Vec16<__nv_bfloat16> {
     static constexpr int N = 8;
     uint4 w;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = __ldcs(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ float amax(float m) const
+    // largest magnitude so far, of the even and of the odd elements (their signs mean nothing); a NaN counts for nothing
+    typedef uint32_t Max;
+    __device__ __forceinline__ void add(Max &m) const
     {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xffff0000u))));
-        return m;
+        for (int i = 0; i < 4; ++i) asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(u[i]));
+    }
+    __device__ __forceinline__ static float value(Max m)
+    {
+        return fmaxf(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xffff0000u)));
     }
     __device__ __forceinline__ void store(uint8_t *p, float f) const
     {
@@ -254,10 +258,12 @@ template <> struct Vec16<float> {
     static constexpr int N = 4;
     float4 w;
     __device__ __forceinline__ void load(const float *p) { w = __ldcs(reinterpret_cast<const float4 *>(p)); }
-    __device__ __forceinline__ float amax(float m) const
+    typedef float Max;
+    __device__ __forceinline__ void add(Max &m) const
     {
-        return fmaxf(fmaxf(m, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(w.z), fabsf(w.w)));
+        m = fmaxf(fmaxf(m, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(w.z), fabsf(w.w)));
     }
+    __device__ __forceinline__ static float value(Max m) { return m; }
     __device__ __forceinline__ void store(uint8_t *p, float f) const
     {
         *reinterpret_cast<uint32_t *>(p) = to_e4m3x4(make_float4(w.x * f, w.y * f, w.z * f, w.w * f));
@@ -302,11 +308,12 @@ __device__ __forceinline__ void append_run(const T *x, int64_t ld, uint8_t *base
     constexpr int E = Vec16<T>::N, C = D / E;
     const float was = off ? *scale : 0.f;
     Vec16<T> y;
-    float mx = 0.f;
+    typename Vec16<T>::Max top = 0;
     for (int r = n - 1; r >= 0; --r) {
         y.load(x + r * ld);
-        mx = y.amax(mx);
+        y.add(top);
     }
+    float mx = Vec16<T>::value(top);
 #pragma unroll
     for (int o = C / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, o));
     const float to = fmaxf(was, scale_of(mx)), inv = 1.f / to;
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append
             const int slot = s_slot[at], pg = slot >> shift, off = slot & (PAGE - 1);
             const T *xr = x + (int64_t)t * ld;
             Vec16<T> y[NP];
-            float mx = 0.f;
+            typename Vec16<T>::Max top = 0;
 #pragma unroll
             for (int i = 0; i < NP; ++i)
                 if (r0 + RH * i < n) y[i].load(xr + (int64_t)(r0 + RH * i) * ld);
@@ -416,7 +423,8 @@ __global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append
             const float was = off ? scale[ph] : 0.f;
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                if (r0 + RH * i < n) mx = y[i].amax(mx);
+                if (r0 + RH * i < n) y[i].add(top);
+            float mx = Vec16<T>::value(top);
 #pragma unroll
             for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             if (GW > 1) {
