@@ -328,8 +328,8 @@ __device__ __forceinline__ void append_run(const T *x, int64_t ld, uint8_t *base
 }
 
 // Threads that hold a page's rows of one head, with four loads of 16 bytes each (the whole CTA with up to 16), and
-// the loads.  (Prompts of 32768 rows of 4 heads, bf16, 128 rows a CTA: pages of 16, d 64: 21 us, and 34 by the CTA with
-// one load a thread; d 128: 35 us with four, and 39 with eight, which leave room for 3 CTAs an SM instead of 5.)
+// the loads.  (Prompts of 32768 rows of 4 heads, bf16, d 64, pages of 16: 21 us, and 34 by the CTA with one load a
+// thread; now 12.7, since the runs' lengths are found once and not by every thread.)
 template <typename T, int D, int PAGE>
 constexpr int HOLD = PAGE * (D / Vec16<T>::N) / 4 < AT ? PAGE * (D / Vec16<T>::N) / 4 : AT;
 template <typename T, int D, int PAGE> constexpr int NPB = PAGE * (D / Vec16<T>::N) / HOLD<T, D, PAGE>;
@@ -343,7 +343,7 @@ template <int N> __device__ __forceinline__ void group_sync(int g)
 }
 
 template <typename T, int D, int PAGE, int TILE>
-__global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append_kernel(const T *__restrict__ k, const T *__restrict__ v,
+__global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 4 : 3) cache_append_kernel(const T *__restrict__ k, const T *__restrict__ v,
                                                           const int32_t *__restrict__ slots, uint8_t *k_cache,
                                                           uint8_t *v_cache, float *k_scale, float *v_scale, int rows,
                                                           int Hk, int num_pages)
@@ -357,7 +357,9 @@ __global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append
     constexpr int SPAN = (TILE + PAGE + 31) & ~31;          // rows looked at
     static_assert(SPAN <= AT, "one row a thread");
     __shared__ uint32_t s_lead[SPAN / 32], s_cont[SPAN / 32];
-    __shared__ int s_slot[TILE];
+    constexpr int TW = (TILE + 31) / 32;
+    __shared__ uint32_t s_short[TW], s_long[TW];            // rows that begin a run of up to kShortRun, of more
+    __shared__ int s_slot[TILE], s_len[TILE];               // and its length
     const int tid = threadIdx.x, lane = tid & 31, c = tid % C, rr = tid / C;
     const int h = blockIdx.y, tile0 = blockIdx.x * TILE;
     const T *x = (blockIdx.z ? v : k) + (int64_t)h * D + E * c;
@@ -392,25 +394,35 @@ __global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append
         }
         return min(n, PAGE - (s_slot[at] & (PAGE - 1)));
     };
-    const uint32_t group = (C == 32 ? 0xffffffffu : (1u << C) - 1) << (lane / C * C);
-    for (int at = rr; at < TILE; at += RP) {
-        if (!leads(at)) continue;
-        const int n = length(at);
-        if (n > kShortRun) continue;
-        const int slot = s_slot[at];
-        const int64_t ph = (int64_t)(slot >> shift) * Hk + h;
-        append_run<T, D>(x + (int64_t)(tile0 + at) * ld, ld, cache + (ph << shift) * D + E * c, scale + ph, n,
-                         slot & (PAGE - 1), c, group);
+    if (tid < 32 * TW) {
+        const int n = tid < TILE && leads(tid) ? length(tid) : 0;
+        if (tid < TILE) s_len[tid] = n;
+        const uint32_t few = __ballot_sync(0xffffffffu, n > 0 && n <= kShortRun), many = __ballot_sync(0xffffffffu, n > kShortRun);
+        if (lane == 0) {
+            s_short[tid >> 5] = few;
+            s_long[tid >> 5] = many;
+        }
     }
-    if (!__syncthreads_or(tid < TILE && leads(tid) && length(tid) > kShortRun)) return;
+    __syncthreads();
+    const uint32_t group = (C == 32 ? 0xffffffffu : (1u << C) - 1) << (lane / C * C);
+    uint32_t any = 0;
+#pragma unroll
+    for (int q = 0; q < TW; ++q) any |= s_short[q];
+    if (any)
+        for (int at = rr; at < TILE; at += RP) {
+            const int n = s_len[at], slot = s_slot[at];
+            if (n == 0 || n > kShortRun) continue;
+            const int64_t ph = (int64_t)(slot >> shift) * Hk + h;
+            append_run<T, D>(x + (int64_t)(tile0 + at) * ld, ld, cache + (ph << shift) * D + E * c, scale + ph, n,
+                             slot & (PAGE - 1), c, group);
+        }
     // group `grp` takes every (AT / GT)-th long run; this thread has a part of its rows r0, r0 + RH, ...
     constexpr int RH = GT / C;
     const int grp = tid / GT, r0 = tid % GT / C;
     int turn = 0;
-    for (int q = 0; q < (TILE + 31) / 32; ++q)
-        for (uint32_t left = s_lead[q]; left; left &= left - 1) {
-            const int at = 32 * q + __ffs(left) - 1, t = tile0 + at, n = length(at);
-            if (n <= kShortRun) continue;
+    for (int q = 0; q < TW; ++q)
+        for (uint32_t left = s_long[q]; left; left &= left - 1) {
+            const int at = 32 * q + __ffs(left) - 1, t = tile0 + at, n = s_len[at];
             if (GT < AT && (turn++ & (AT / GT - 1)) != grp) continue;
             const int slot = s_slot[at], pg = slot >> shift, off = slot & (PAGE - 1);
             const T *xr = x + (int64_t)t * ld;
@@ -449,10 +461,11 @@ __global__ void __launch_bounds__(AT, NPB<T, D, PAGE> <= 4 ? 5 : 3) cache_append
 template <typename T, int D, int PAGE> cudaError_t run_append(const CacheAppendArgs &a, cudaStream_t st)
 {
     // Rows a CTA: few where rows are few, so that a generation step's spread over the SMs (256 rows of 4 heads,
-    // d 128, page 64, bf16: 2.5 us with 16, 5.3 with 64), more where they are many (prompts of 32768 rows, d 64:
-    // 30 us with 16, 22 with 64, 17 with 128, for 7.8 at the copy rate), but 64 where they all fit the SMs at once
-    // (4096 rows, d 64: 4.3 us with 64, 4.7 with 128; d 128: 5.0 and 6.0).
-    const int tile = a.rows <= 2048 ? 16 : (long)a.rows / 64 * a.Hk * 2 <= 5 * 148 ? 64 : 128;
+    // d 128, page 64, bf16: 2.3 us with 16, 5.3 with 64), more where they are many (prompts of 32768 rows, d 64:
+    // 30 us with 16, 22 with 64, 17 with 128 when that was measured, now 11.2, for 7.8 at the copy rate), but 64 where
+    // they all fit the SMs at once (4096 rows, d 64: 4.3 us with 64, 4.7 with 128; d 128: 5.0 and 6.0).  Four CTAs an
+    // SM: with five, registers spill (8192 rows of a step, d 128: 13.5 us with four, 17.8 with five).
+    const int tile = a.rows <= 2048 ? 16 : (long)a.rows / 64 * a.Hk * 2 <= 4 * 148 ? 64 : 128;
     auto kern = tile == 16 ? cache_append_kernel<T, D, PAGE, 16> : tile == 64 ? cache_append_kernel<T, D, PAGE, 64>
                                                                              : cache_append_kernel<T, D, PAGE, 128>;
     kern<<<dim3((a.rows + tile - 1) / tile, a.Hk, 2), AT, 0, st>>>((const T *)a.k, (const T *)a.v, a.slots, a.k_cache,
