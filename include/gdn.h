@@ -492,8 +492,9 @@ GDN_API int gdn_cache_append(const void *k, const void *v, const int32_t *slots,
  * table entry is outside 0 .. num_pages - 1 are left out.  Cache contents beyond a request's length
  * are never part of a result, whatever they are.  Cached values enter the tensor cores as fp16
  * (exact), q as fp16 after a power-of-two scaling of each head (bf16 exact over 22 binary orders;
- * fp32 as a sum of two fp16), softmax weights as fp16 (bf16 calls) or a sum of two fp16 (fp32 calls), sums in
- * fp32.  d in {64, 128}; scale finite and > 0.  Workspace: gdn_attn_decode_workspace_bytes(...)
+ * fp32 as a sum of two fp16), softmax weights as fp16 (bf16 calls: off by at most 2^-11) or a sum of two fp16 (fp32
+ * calls: 2^-22), sums in fp32.  A weight far below the largest, each times its page's value scale, is off by up
+ * to 2^-39 of that largest one, if not by itself.  d in {64, 128}; scale finite and > 0.  Workspace: gdn_attn_decode_workspace_bytes(...)
  * bytes, 256-byte aligned (long contexts are split over CTAs; may be NULL when that is 0).
  */
 GDN_API int gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,

@@ -16,8 +16,13 @@
 // (online softmax), and the four warps join at the end.  A long context is split over CTAs whose
 // partial results a second kernel joins.
 //
-// The weights' frame: p_j = exp2(s_j + log2 vs_j - M), M = max_j (s_j + log2 vs_j), so that
-// p_j V8_j needs no further scale and p <= 1 fits fp16; the softmax sum takes p_j / vs_j.
+// The weights' frame: p_j = 2^15 exp2(s_j + log2 vs_j - M), M the least whole number at or above every
+// s_j + log2 vs_j, so that p_j V8_j needs no further scale; the softmax sum takes p_j / vs_j.  p_j is rounded to fp16
+// for the product (a half step of 2^-11 against bf16's 2^-8, and V8 must be fp16 beside it), and in an fp32 call to
+// the sum of two fp16 (2^-22).  2^15 uses all of fp16's range: the largest weight lies in (2^14, 2^15], and what
+// falls below fp16's normal numbers is off by 2^-39 of it at most; with the largest at 1 that floor was 2^-25, and
+// 8192 tokens behind one that draws 2^24 of their weight and has a value of 0 came out 6e-3 (fp32 calls) to 1e-1 off.
+// M is whole so that moving it (powers of two) and taking 15 from it are exact.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -42,6 +47,7 @@ constexpr int NSTG = 2;   // ring stages per warp
 constexpr int OCC = 3;    // CTAs per SM: while one starts (a chain of dependent loads) the others stream (256 ragged
                           // contexts: 301 us; with two CTAs of three stages 319)
 constexpr int JW = 16;    // warps of the join
+constexpr float kFrame = 15.f;  // log2 of the largest weight in its frame (above)
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(NW * 32, OCC)
                 for (int e = 0; e < 2; ++e) {
 #pragma unroll
                     for (int b = 4; b < 32; b <<= 1) mx[x][e] = fmaxf(mx[x][e], __shfl_xor_sync(0xffffffffu, mx[x][e], b));
-                    const float to = fmaxf(m[x][e], mx[x][e]);
+                    const float to = fmaxf(m[x][e], ceilf(mx[x][e]));
                     const float f = to == -INFINITY ? 1.f : ex2_approx(m[x][e] - to);
                     m[x][e] = to;
                     l[x][e] *= f;
@@ -507,7 +513,7 @@ __global__ void __launch_bounds__(NW * 32, OCC)
         uint32_t pb[NQ][2][2];  // weights as B operands of 16 tokens: the groups, or the weights' two parts
 #pragma unroll
         for (int x = 0; x < NA; ++x) {
-            const float b0 = m[x][0] == -INFINITY ? 0.f : m[x][0], b1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
+            const float b0 = m[x][0] == -INFINITY ? 0.f : m[x][0] - kFrame, b1 = m[x][1] == -INFINITY ? 0.f : m[x][1] - kFrame;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
