@@ -33,6 +33,8 @@ cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t stream);
 cudaError_t launch_attn_bwd_simt(const AttnArgs &a, cudaStream_t stream);
 size_t attn_bwd_simt_workspace(int B, int T, int Hq, int Hk, int d, int varlen);
 
+constexpr int kMaxPlan = 16384;  // requests of a plan
+
 struct CachePlanArgs {
     const int32_t *lens, *added;
     int32_t *table;

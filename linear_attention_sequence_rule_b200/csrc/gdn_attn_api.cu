@@ -149,7 +149,7 @@ int gdn_cache_plan(const int32_t *lens, const int32_t *added, int32_t *block_tab
     set_error("%s", "");
     int rc = check_page(fn, page);
     if (rc != GDN_OK) return rc;
-    if (N > 16384) return refuse(GDN_ERR_UNSUPPORTED, "%s: N=%d, supported: up to 16384", fn, N);
+    if (N > kMaxPlan) return refuse(GDN_ERR_UNSUPPORTED, "%s: N=%d, supported: up to %d", fn, N, kMaxPlan);
     if (N < 1 || max_blocks < 1 || num_free < 0 || rows < 0 || rows > (1 << 30) || (long long)max_blocks * page >= (1LL << 31))
         return refuse(GDN_ERR_INVALID_ARGUMENT, "%s: N=%d max_blocks=%d num_free=%d rows=%d out of range", fn, N,
                       max_blocks, num_free, rows);

@@ -486,9 +486,12 @@ template <typename T, int D> cudaError_t run_append(const CacheAppendArgs &a, cu
 
 cudaError_t launch_cache_plan(const CachePlanArgs &a, cudaStream_t st)
 {
-    const int smem = (3 * a.N + 1) * 4;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // Without leave a CTA has 48 KB, the kernel's static arrays (some 500 bytes) among them.  The leave is the kernel's,
+    // not the call's: always the largest plan's, so that a call beside this one cannot lower it before the launch.
+    auto bytes = [](int n) { return (3 * n + 1) * 4; };
+    const int smem = bytes(a.N);
+    if (smem > 47 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxPlan));
         if (e != cudaSuccess) return e;
     }
     cache_plan_kernel<<<PC, PT, smem, st>>>(a);
