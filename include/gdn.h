@@ -442,8 +442,8 @@ GDN_API size_t gdn_attn_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d,
  *        b page .. b page + page - 1.  Entries of pages already held are read, those of the pages
  *        taken now are written, all others are left as they were.
  *   out: cu_seqlens [N+1]: offsets of the requests' new tokens in the step's packed rows;
- *        slots [rows]: page number x page + offset of every new token, positions [rows]: its
- *        position in its request; both -1 in rows behind cu_seqlens[N]
+ *        slots [rows]: page number x page + offset of every new token (-1 where 32 bits do not hold
+ *        it), positions [rows]: its position in its request; both -1 in rows behind cu_seqlens[N]
  *        lens_out [N] = lens + added, free_head_out [1] (each may be the input array itself)
  *        status [2]: {0, 0}; or why the whole plan was refused, in which case no page is taken, the
  *        table is left, cu_seqlens is all 0, slots and positions all -1, lens_out = lens and

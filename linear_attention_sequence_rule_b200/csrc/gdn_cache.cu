@@ -173,7 +173,9 @@ __global__ void __cluster_dims__(PC, 1, 1) __launch_bounds__(PT) cache_plan_kern
                     block = b;
                 }
                 pos[e] = p;
-                slot[e] = page_no * a.page + (p & (a.page - 1));
+                // a page number too large for a slot of 32 bits must not come out as another page's
+                const int first = (int)((uint32_t)page_no << shift);
+                slot[e] = first >> shift == page_no ? first + (p & (a.page - 1)) : -1;
             }
         }
         if (t0 + 3 < a.rows) {

@@ -1,5 +1,5 @@
-"""Plans of every number of requests, in a process that has planned nothing larger before, and plans of different sizes
-from two host threads at once."""
+"""Plans of every number of requests, in a process that has planned nothing larger before, plans of different sizes
+from host threads at once, and page numbers of every size."""
 import os
 import subprocess
 import sys
@@ -78,3 +78,21 @@ def test_two_host_threads_plan_batches_of_different_sizes():
     for t in threads:
         t.join()
     assert not faults, faults
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_page_numbers_that_no_slot_holds(page):
+    """A slot is page number x page + offset, or -1 where 32 bits do not hold it: never a slot of another page."""
+    import linear_attention_sequence_rule_b200 as gdn
+    top = 2 ** 31 // page
+    numbers = [0, 5, -1, -2, top - 1, top, top + 3, 2 * top, 2 * top + 1, 2 ** 31 - 1, -top, -top - 1, -2 * top, -2 ** 31]
+    n = len(numbers)
+    t = i32([[x, -1] for x in numbers])  # every request holds three tokens and fills its page, then takes one
+    p = gdn.cache_plan(i32([3] * n), i32([page - 2] * n), t, i32(numbers), i32([0]), page, n * (page - 2))
+    assert p.status.tolist() == [0, 0]
+    want = []
+    for x in numbers:
+        slots = [x * page + j for j in range(3, page)] + [x * page]
+        want += [s if -2 ** 31 <= s < 2 ** 31 else -1 for s in slots]
+    assert p.slots.tolist() == want and t[:, 1].tolist() == numbers
+    assert p.positions.tolist() == list(range(3, page + 1)) * n
