@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(NTH, 1)
         const int jd = 2 * (2 * at.block + t);  // first step of the diagonal block
         float m = -INFINITY, l = 0.f;           // m in units of S
         auto fetch = [&](int j, float (&x)[2][32]) {
-            w.wait(&bar[C::s_full + C::NB * t + j % C::NB], j / C::NB);
+            w.wait_warp(&bar[C::s_full + C::NB * t + j % C::NB], j / C::NB);
             tc_fence_after();
             tmem_ld32(tS + HT * (j % C::NB), x[0]);
             tmem_ld32(tS + HT * (j % C::NB) + 32, x[1]);
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 m = to;
                 l *= f;
                 if (j > 0) {  // once O is at rest
-                    w.wait(&bar[C::pv_done + 2 * t + ((j - 1) & 1)], (j - 1) >> 1);
+                    w.wait_warp(&bar[C::pv_done + 2 * t + ((j - 1) & 1)], (j - 1) >> 1);
                     tc_fence_after();
 #pragma unroll
                     for (int x = 0; x < D / 32; ++x) {
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 step(j, x, y);
                 if (j + 1 < n) step(j + 1, y, x);
             }
-            w.wait(&bar[C::all_done + t], 0);
+            w.wait_warp(&bar[C::all_done + t], 0);
             tc_fence_after();
             if (!w.stopped()) {
                 const int64_t row0 = at.t0 + q0 + t * BT;

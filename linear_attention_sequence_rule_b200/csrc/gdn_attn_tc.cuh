@@ -54,6 +54,13 @@ struct Waits {
             }
         }
     }
+    // the same for a whole warp ahead of an instruction that its lanes must execute together (tensor memory's loads and
+    // stores): lanes that found the phase over at different probes meet again here
+    __device__ __forceinline__ void wait_warp(uint64_t *b, int phase) const
+    {
+        wait(b, phase);
+        __syncwarp();
+    }
 };
 
 __device__ __forceinline__ void arrive(uint64_t *b)

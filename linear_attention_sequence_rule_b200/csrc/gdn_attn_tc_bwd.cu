@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(NTH, 1)
                 if (x < rows) ov[u] = *(reinterpret_cast<const uint4 *>(out + ((row0 + x) * Hq + h) * D) + un);
             }
         }
-        w.wait(&bar[C::q_full], 0);  // groups 0, 1: halves of Q's rows, 2, 3: of dO's
+        w.wait_warp(&bar[C::q_full], 0);  // groups 0, 1: halves of Q's rows, 2, 3: of dO's
         row_to_tmem<D / 2>(tmem + lanes + (g < 2 ? C::tQ : C::tO), sm + (g < 2 ? C::Q : C::O), r, (g & 1) * (D / 2));
         tmem_wait_st();
         tc_fence_before();
@@ -354,8 +354,7 @@ __global__ void __launch_bounds__(NTH, 1)
             const int key0 = (i < n ? i : i - n) * HT + c0 - at.block * BT;  // of this thread's columns, as r counts
             const uint32_t tS = tmem + lanes + C::tS + HT * ts.tile() + c0, tP = tmem + lanes + C::tP + HT * tp.tile() + c0;
             float s[32], dp[32];
-            w.wait(&bar[C::s_full + ts.b], ts.ph);
-            __syncwarp();
+            w.wait_warp(&bar[C::s_full + ts.b], ts.ph);
             tc_fence_after();
             tmem_ld32(tS, s);
             if (C::BOTH) tmem_ld32(tP, dp);
@@ -376,7 +375,7 @@ __global__ void __launch_bounds__(NTH, 1)
                     if (key0 + x > r) s[x] = 0.f;
             }
             if (!C::BOTH) {
-                w.wait(&bar[C::dp_full + tp.b], tp.ph);
+                w.wait_warp(&bar[C::dp_full + tp.b], tp.ph);
                 tc_fence_after();
                 tmem_ld32(tP, dp);
                 tmem_wait_ld();
@@ -404,7 +403,7 @@ __global__ void __launch_bounds__(NTH, 1)
         }
         if (!joined) join();  // no step in the second pass, or left early: the other warps still come by
         if (!w.stopped()) {
-            w.wait(&bar[C::all_done], 0);
+            w.wait_warp(&bar[C::all_done], 0);
             tc_fence_after();
             if (!w.stopped() && g < 2)
                 store_rows<D, D / 2>(tmem + lanes + C::tG, scale, sm + C::Q, wq, lane, g * (D / 2),
@@ -625,8 +624,7 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             const uint32_t tS = tmem + lanes + C::tS + HT * ts.tile() + c0, tP = tmem + lanes + C::tP + HT * tp.tile() + c0;
             float p[32], dp[32];
             w.wait(&bar[C::s_full + ts.b], ts.ph);
-            w.wait(&bar[C::q_full + s], j / NS);  // over by now: for the rows' -lse and -D
-            __syncwarp();
+            w.wait_warp(&bar[C::q_full + s], j / NS);  // over by now: for the rows' -lse and -D
             tc_fence_after();
             tmem_ld32(tS, p);
             tmem_wait_ld();
@@ -653,7 +651,7 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&bar[C::p_full + ts.b], lane);
-            w.wait(&bar[C::dp_full + tp.b], tp.ph);
+            w.wait_warp(&bar[C::dp_full + tp.b], tp.ph);
             tc_fence_after();
             tmem_ld32(tP, dp);
             tmem_wait_ld();
@@ -673,7 +671,7 @@ __global__ void __launch_bounds__(NTH_KEY, 1)
             warp_arrive(&bar[C::ds_full + tp.b], lane);
         }
         if (!w.stopped()) {
-            w.wait(&bar[C::all_done], 0);
+            w.wait_warp(&bar[C::all_done], 0);
             tc_fence_after();
             if (!w.stopped()) {  // groups 0 and 1 store dV, 2 and 3 dK
                 __nv_bfloat16 *to = (g >= 2 ? dk : dv) + (row0 * Hk + hk) * D;
