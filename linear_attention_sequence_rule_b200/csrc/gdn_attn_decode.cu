@@ -718,15 +718,15 @@ bool cache_map(CUtensorMap *m, const void *base, int num_pages, int Hk, int page
 
 template <int D, int KIND> cudaError_t run_decode(const AttnDecodeArgs &a, cudaStream_t st)
 {
-    CUtensorMap mk, mv;
-    if (!cache_map(&mk, a.k_cache, a.num_pages, a.Hk, a.page, D) || !cache_map(&mv, a.v_cache, a.num_pages, a.Hk, a.page, D))
-        return cudaErrorInvalidValue;
     const int mtiles = head_tiles(a.Hq / a.Hk, a.dtype);
     const int splits = split_count(a.N, a.Hk, mtiles, a.page, a.max_blocks);
     constexpr int smem = decode_smem<D>();
     auto kern = attn_decode_kernel<D, KIND>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    CUtensorMap mk, mv;
+    if (!cache_map(&mk, a.k_cache, a.num_pages, a.Hk, a.page, D) || !cache_map(&mv, a.v_cache, a.num_pages, a.Hk, a.page, D))
+        return cudaErrorInvalidValue;
     const long ctas = (long)a.N * a.Hk * mtiles * splits;
     const int ordered = a.N > 1 && a.N <= kOrdered && (long)a.max_blocks * a.page >= kOrderedFrom && ctas > (long)OCC * sm_count();
     kern<<<(unsigned)ctas, NW * 32, smem, st>>>(mk, mv, a, splits, mtiles, ordered);

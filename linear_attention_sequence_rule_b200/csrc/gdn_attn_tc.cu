@@ -306,11 +306,11 @@ template <int D> cudaError_t run_fwd(const AttnArgs &a, cudaStream_t st)
 {
     using C = FwdCfg<D>;
     const int64_t tokens = a.cu ? (int64_t)a.T : (int64_t)a.B * a.T;
+    cudaError_t e = cudaFuncSetAttribute(attn_fwd_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
+    if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, a.q, tokens, a.Hq, D) || !make_map(&mk, a.k, tokens, a.Hk, D) || !make_map(&mv, a.v, tokens, a.Hk, D))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attn_fwd_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
-    if (e != cudaSuccess) return e;
     const long tiles = attn_tiles(a.cu, a.B, a.T, 2 * BT);
     attn_fwd_tc<D><<<(unsigned)(tiles * a.Hq), NTH, C::TOTAL, st>>>(mq, mk, mv, static_cast<__nv_bfloat16 *>(a.out), a.lse,
                                                                    a.cu, FastDiv(a.B), a.T, FastDiv(a.Hq), FastDiv(a.Hq / a.Hk),

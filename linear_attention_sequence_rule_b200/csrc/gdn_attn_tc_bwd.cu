@@ -697,14 +697,14 @@ template <int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t st)
     using A = DqCfg<D>;
     using Bc = DkvCfg<D>;
     const int64_t tokens = a.cu ? (int64_t)a.T : (int64_t)a.B * a.T;
-    CUtensorMap mq, mk, mv, mo;
-    if (!make_map(&mq, a.q, tokens, a.Hq, D) || !make_map(&mk, a.k, tokens, a.Hk, D) ||
-        !make_map(&mv, a.v, tokens, a.Hk, D) || !make_map(&mo, a.dout, tokens, a.Hq, D))
-        return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(attn_bwd_dq_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::TOTAL);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attn_bwd_dkv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Bc::TOTAL);
     if (e != cudaSuccess) return e;
+    CUtensorMap mq, mk, mv, mo;
+    if (!make_map(&mq, a.q, tokens, a.Hq, D) || !make_map(&mk, a.k, tokens, a.Hk, D) ||
+        !make_map(&mv, a.v, tokens, a.Hk, D) || !make_map(&mo, a.dout, tokens, a.Hq, D))
+        return cudaErrorInvalidValue;
     float *nlse = static_cast<float *>(a.workspace), *ndot = nlse + tokens * a.Hq;
     const long tiles = attn_tiles(a.cu, a.B, a.T, BT);
     const int G = a.Hq / a.Hk;

@@ -7,6 +7,8 @@
 
 namespace gdn {
 
+// The encoder refuses a host thread without a current context, and a thread's first call of this library may be its first
+// of CUDA: callers make a runtime call that needs the context (the kernel's attribute) before they encode.
 inline PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder()
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
