@@ -1372,23 +1372,7 @@ template <int DK, int DV>
 cudaError_t launch_tc(const TcLaunch &a, cudaStream_t st)
 {
     using L = TcCfg<DK, DV>;
-    CUtensorMap mq, mk, mv;
-    // a zero-token varlen call still launches so that S_final = S0 is written
-    const long map_tokens = a.tokens > 0 ? a.tokens : 1;
-    // with V taken as zero nothing is loaded through the V map; any valid map will do
-    // with V taken as zero the V map is never read: the k map (H / G heads) serves as a stand-in
-    const void *vsrc = (a.flags & kFlagVZero) ? a.k : a.v;
-    const int vdim = (a.flags & kFlagVZero) ? DK : DV * a.vblocks;
-    const int vheads = (a.flags & kFlagVZero) ? a.H / a.G : a.H;
     const bool ph = (a.flags & kFlagPhase) != 0;
-    const bool qk_ok = ph ? make_map_f32(&mq, a.q, map_tokens, a.H / a.G, DK) &&
-                                make_map_f32(&mk, a.k, map_tokens, a.H / a.G, DK)
-                          : make_map(&mq, a.q, map_tokens, a.H / a.G, DK) &&
-                                make_map(&mk, a.k, map_tokens, a.H / a.G, DK);
-    if (!qk_ok || !make_map(&mv, vsrc, map_tokens, vheads, vdim)) {
-        set_error("cuTensorMapEncodeTiled failed");
-        return cudaErrorInvalidValue;
-    }
     int smem = L::TOTAL + 1024;
     auto kern = (a.flags & kFlagPrologue) ? chunk_tc_kernel<DK, DV, true> : chunk_tc_kernel<DK, DV, false>;
     if constexpr (DK == 64 && DV == 64) {
@@ -1400,8 +1384,25 @@ cudaError_t launch_tc(const TcLaunch &a, cudaStream_t st)
         set_error("the fused phase prologue runs at head size 64, value head 64 only");
         return cudaErrorInvalidValue;
     }
+    // ahead of the tensor maps: the encoder refuses a host thread whose context no runtime call has made current yet
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    CUtensorMap mq, mk, mv;
+    // a zero-token varlen call still launches so that S_final = S0 is written
+    const long map_tokens = a.tokens > 0 ? a.tokens : 1;
+    // with V taken as zero nothing is loaded through the V map; any valid map will do
+    // with V taken as zero the V map is never read: the k map (H / G heads) serves as a stand-in
+    const void *vsrc = (a.flags & kFlagVZero) ? a.k : a.v;
+    const int vdim = (a.flags & kFlagVZero) ? DK : DV * a.vblocks;
+    const int vheads = (a.flags & kFlagVZero) ? a.H / a.G : a.H;
+    const bool qk_ok = ph ? make_map_f32(&mq, a.q, map_tokens, a.H / a.G, DK) &&
+                                make_map_f32(&mk, a.k, map_tokens, a.H / a.G, DK)
+                          : make_map(&mq, a.q, map_tokens, a.H / a.G, DK) &&
+                                make_map(&mk, a.k, map_tokens, a.H / a.G, DK);
+    if (!qk_ok || !make_map(&mv, vsrc, map_tokens, vheads, vdim)) {
+        set_error("cuTensorMapEncodeTiled failed");
+        return cudaErrorInvalidValue;
+    }
     const dim3 grid(a.vblocks, a.H, a.nseq);
     kern<<<grid, L::THREADS, smem, st>>>(mq, mk, mv, a.log_alpha, a.beta, a.S0,
                                        static_cast<__nv_bfloat16 *>(a.out), a.S_final, a.cu, a.T, a.H,

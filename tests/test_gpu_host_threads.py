@@ -86,3 +86,22 @@ def test_generation_step(dtype):
     for fn in calls(got):
         assert in_a_new_thread(fn) == (gdn.GDN_OK, "")
     assert want["status"].tolist() == [0, 0] and all(torch.equal(got[x], want[x]) for x in want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_chunk_forward(dtype):
+    import linear_attention_sequence_rule_b200 as gdn
+    T, H, d, code = 200, 2, 64, gdn._DT[DT[dtype]]
+    g = torch.Generator("cuda").manual_seed(2)
+    q, k, v = (torch.nn.functional.normalize(torch.randn(1, T, H, d, generator=g, device="cuda"), dim=-1).to(DT[dtype])
+               for _ in range(3))
+    la, be = -0.1 * torch.rand(1, T, H, generator=g, device="cuda"), torch.rand(1, T, H, generator=g, device="cuda")
+    want = gdn.chunk_fwd(q, k, v, la, be)
+    got = [torch.zeros_like(x) for x in want]
+    ws = torch.empty(max(256, gdn.gdn_chunk_fwd_workspace_bytes(1, T, H, d, d, 64, 0, code)), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    ins, outs = [x.data_ptr() for x in (q, k, v, la, be)], [x.data_ptr() for x in got]
+    pw, n = ws.data_ptr(), ws.numel()
+    rc = in_a_new_thread(lambda: gdn.gdn_chunk_fwd(*ins, None, *outs, 1, T, H, d, d, 64, None, code, pw, n, 0))
+    assert rc == (gdn.GDN_OK, "")
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
