@@ -687,8 +687,8 @@ int head_tiles(int G, int dtype)
 
 // Splits of a context.  A CTA starts with a chain of dependent loads, some 5 us, so splits beyond need cost:
 // - few (request, key head) pairs: one CTA for each place on the SMs, down to a tile a warp (one context of
-//   65536 tokens, 4 key heads: 19.3 us in 111 splits, 20.4 in 55, 26 in 27, 25 in 222; of 4096: 7.2 us in 32
-//   splits, 8.2 in 27);
+//   65536 tokens, 4 key heads, its cache in L2: 19.3 us in 111 splits, 20.4 in 55, 26 in 27, 25 in 222; now 18.1 in 111,
+//   and 22.5 from HBM; of 4096: 7.2 us in 32 splits, 8.2 in 27);
 // - more: about 1.5 for each place, down to two tiles a warp (contexts of 128 to 8192 tokens, 8 key heads: 16 of
 //   them 34.7 us in 6 splits, 37.9 in 8, 34.8 in 4; 32 of them 56.4 in 3, 59.7 in 4, 57.9 in 2);
 // - pairs for all places: two splits only where they leave 16 tiles a warp (64 contexts of 128 to 8192 tokens, 8

@@ -10,8 +10,12 @@
 // over the S it came from.  So the scores of the next steps are formed while a step's softmax runs; with
 // one S tile of 128 keys a query tile had only one of the two under way, and a step of 128 keys took
 // 4500 cycles for 2048 of products or exponentials.
-// 16384 tokens, 16 heads on 4: 0.84 ms at d = 128 (1310 TFLOP/s, 78 % of what a large plain product reaches) and
-// 0.71 ms at d = 64, where the exponentials, 16 a cycle and SM, take 0.47 ms at full clocks and the products less.
+// 16384 tokens, 16 heads on 4: 0.84-0.87 ms at d = 128 (1310-1260 TFLOP/s, 78-75 % of what a large plain product
+// reaches; 1.01 ms in a long run under the power cap) and 0.73-0.76 ms at d = 64, where the exponentials, 16 a
+// cycle and SM, take 0.47 ms at full clocks and the products less.
+// P is rounded to bf16 for its product: both operands of a product have one type, and V is bf16 (P as a sum of two would
+// double the product).  l sums the weights unrounded, in fp32.  The result is off by 2.0e-3 (relative, root mean square),
+// 1.7e-3 of it from its own rounding.
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread holds a row
 //   warps 8, 9       issue the MMAs of tile 0, 1
 //   warp 10          loads; zeroes V rows behind the sequence's end

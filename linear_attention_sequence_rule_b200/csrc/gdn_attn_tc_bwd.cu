@@ -10,18 +10,20 @@
 // summed in tensor memory by one CTA in one order: no atomics, no partial sums in HBM, a call repeats
 // bit for bit.
 //
-// D from the rounded result is off by 2^-9 |dO| |O|, which counts where few keys carry a row: a row
-// that sees one key has dS = 0, and what is left is that error.  The first kExactBlocks query
-// blocks of a sequence therefore form D as sum_j P_ij dP_ij in a pass of their own; behind them rows
-// average over more keys, and D is taken from out.  The query side writes D and -lse log2 e for
-// the key side, head by head ([Hq][tokens] each), into the workspace.
+// D from the rounded result is off by up to 2^-8 sum |dO| |O|, which counts where dS is small beside D: a row of few keys, or
+// of values that lie near one another.  The first kExactBlocks query blocks of a sequence, where rows have few keys,
+// therefore form D as sum_j P_ij dP_ij in a pass of their own (for every block that would be a pass of two products more
+// than the three of the query side); behind them D is taken from out as it was rounded.  The query side writes D and
+// -lse log2 e for the key side, head by head ([Hq][tokens] each), into the workspace.
+// P and dS are rounded to bf16 for their products: both operands of a product have one type, and Q, K and dO are bf16.
+// Gradients are off by 2.3e-3 (relative, root mean square), 1.7e-3 of it from their own rounding.
 //
 // Both kernels work in steps of 64 keys (query side) or 64 queries (key side): 128 x 64 tiles of S and
 // dP in tensor memory beside the gradients, two of each at d = 128 (2 x 64 + 2 x 64 + 256 columns) and three at
 // d = 64, so that the products of the next steps run while a step's elements are worked on.  What bounds them is
-// the chain of waits between products and elements: at d = 64 (16384 tokens, 16 heads) the query side takes
-// 0.88 ms, 0.80 without its exponentials, 0.75 without any product, and still 0.53 without both and the rest of the
-// element-wise work.  Steps of 128 with one dP (or, on the key side, one S) tile spend half their time on it, and
+// the chain of waits between products and elements: at d = 64 (16384 tokens, 16 heads) the query side, when it took
+// 0.88 ms (0.82 now), took 0.80 without its exponentials, 0.75 without any product, and still 0.53 without both and
+// the rest of the element-wise work.  Steps of 128 with one dP (or, on the key side, one S) tile spend half their time on it, and
 // half again as many element-wise warps change nothing.
 // A product 64 wide of two shared operands takes 48 cycles for 32 cycles' work, so the query side moves Q and dO
 // to tensor memory.  The key side leaves K and V in shared memory: at d = 64 a third tile of S and dP gives more
@@ -30,7 +32,7 @@
 // A CTA's start and end cost some 5 us (setting up, the first loads, a chain of products and elements with nothing
 // beside it, the results), a quarter of its time at 4096 tokens; CTAs that take one tile after another
 // instead of being launched anew were no faster.
-// 16384 tokens, 16 heads on 4: query side 1.17 ms at d = 128 and 0.83 at d = 64, key side 1.63 and 1.00 ms.
+// 16384 tokens, 16 heads on 4: query side 1.17 ms at d = 128 and 0.82 at d = 64, key side 1.64 and 1.00 ms.
 //   warps 0-7, 8-15  element by element, the even and the odd steps: a thread has a row, 32 columns
 //   warps 16-18      issue the products (key side: 16-19; one product a warp, since its waits and commits
 //                    take longer than the product)

@@ -331,7 +331,8 @@ __device__ __forceinline__ void append_run(const T *x, int64_t ld, uint8_t *base
 
 // Threads that hold a page's rows of one head, with four loads of 16 bytes each (the whole CTA with up to 16), and
 // the loads.  (Prompts of 32768 rows of 4 heads, bf16, d 64, pages of 16: 21 us, and 34 by the CTA with one load a
-// thread; now 12.7, since the runs' lengths are found once and not by every thread.)
+// thread; now 12.7, since the runs' lengths are found once and not by every thread; all with the rows in L2, from HBM
+// now 16.7.)
 template <typename T, int D, int PAGE>
 constexpr int HOLD = PAGE * (D / Vec16<T>::N) / 4 < AT ? PAGE * (D / Vec16<T>::N) / 4 : AT;
 template <typename T, int D, int PAGE> constexpr int NPB = PAGE * (D / Vec16<T>::N) / HOLD<T, D, PAGE>;
@@ -464,7 +465,7 @@ template <typename T, int D, int PAGE> cudaError_t run_append(const CacheAppendA
 {
     // Rows a CTA: few where rows are few, so that a generation step's spread over the SMs (256 rows of 4 heads,
     // d 128, page 64, bf16: 2.3 us with 16, 5.3 with 64), more where they are many (prompts of 32768 rows, d 64:
-    // 30 us with 16, 22 with 64, 17 with 128 when that was measured, now 11.2, for 7.8 at the copy rate), but 64 where
+    // 30 us with 16, 22 with 64, 17 with 128 when that was measured, now 11.2, the rows in L2), but 64 where
     // they all fit the SMs at once (4096 rows, d 64: 4.3 us with 64, 4.7 with 128; d 128: 5.0 and 6.0).  Four CTAs an
     // SM: with five, registers spill (8192 rows of a step, d 128: 13.5 us with four, 17.8 with five).
     const int tile = a.rows <= 2048 ? 16 : (long)a.rows / 64 * a.Hk * 2 <= 4 * 148 ? 64 : 128;
